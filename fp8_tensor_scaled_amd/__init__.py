@@ -24,6 +24,8 @@ __all__ = [
     "fp8_linear_fwd", "fp8_linear_bwd", "fp8_linear_fwd_workspace",
     "fp8_linear_bwd_workspace", "fp8_linear_bwd_workspace_codes", "fp8_linear_fwd_x8_offset",
     "fp8_linear_fwd_w8_offset",
+    "GROUP_LINE", "GROUP_TILE", "fp8_quantize_block", "fp8_mm_block", "fp8_mm_block_workspace",
+    "fp8_moe", "fp8_moe_workspace",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -43,6 +45,8 @@ EXPORTED_SYMBOLS = (
     "fp8_quantize_colsum_noalloc", "fp8_linear_fwd_workspace",
     "fp8_linear_fwd_x8_offset", "fp8_linear_fwd_w8_offset", "fp8_linear_fwd",
     "fp8_linear_bwd_workspace", "fp8_linear_bwd_workspace_codes", "fp8_linear_bwd",
+    "fp8_quantize_block", "fp8_mm_block_workspace", "fp8_mm_block", "fp8_moe_workspace",
+    "fp8_moe",
     "fp8_last_error", "fp8_version",
 )
 
@@ -102,6 +106,12 @@ def _load() -> ctypes.CDLL:
         "fp8_linear_bwd_workspace_codes": (S, [I64, I64, I64]),
         "fp8_linear_bwd": (I32, [P, P, P, I64, I64, I64, I32, I32, I32, P, R, P, S, P, P, P, P,
                                  P, P, P]),
+        "fp8_quantize_block": (I32, [P, I32, I64, I64, I64, I32, I32, P, P, P, P, P, P, P]),
+        "fp8_mm_block_workspace": (S, [I64, I64, I64]),
+        "fp8_mm_block": (I32, [P, P, I32, I32, I32, I32, I64, I64, I64, I64, I64, P, I32, P, I32,
+                               P, P, P, S, P]),
+        "fp8_moe_workspace": (S, [I64, I64, I64, I64, I64]),
+        "fp8_moe": (I32, [P, P, P, P, P, P, I64, I64, I64, I64, I64, I32, I32, P, S, P, P, P, P]),
         "fp8_last_error": (ctypes.c_char_p, []),
         "fp8_version": (ctypes.c_char_p, []),
     }
@@ -570,3 +580,137 @@ def _linear_bwd_call(g, x, w, M, N, K, fmt, dynamic, margin, scales_fwd, ring_g,
                              _ptr(dw), _ptr(db),
                              _ptr(x8_bwd), _ptr(w8_bwd), _stream(stream))
     _check(st, "fp8_linear_bwd")
+
+
+# --------------------------------------------------------------------------
+# Block scaling: one step for each group of 128 values
+# --------------------------------------------------------------------------
+
+# Groupings of an operand of fp8_mm_block (fp8_group_t).
+GROUP_LINE, GROUP_TILE = 0, 1
+BLOCK = 128
+_BF16 = tuple(d for d in _BYTE2 if d != torch.float16)  # bf16 values or their bit patterns
+
+
+def _groups(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def fp8_quantize_block(x: torch.Tensor, rows: int, cols: int, fmt: int,
+                       out_row: torch.Tensor | None = None,
+                       scale_row: torch.Tensor | None = None,
+                       out_col: torch.Tensor | None = None,
+                       scale_col: torch.Tensor | None = None,
+                       out_tile: torch.Tensor | None = None,
+                       scale_tile: torch.Tensor | None = None, margin: int = 0,
+                       ldx: int | None = None, in_type: int | None = None, stream=None) -> None:
+    """bf16, fp16 or fp32 x [rows][cols] -> fp8 codes with a step for each
+    group of 128: along rows (``out_row``, ``scale_row``
+    [rows][ceil(cols/128)]), along columns (``out_col``, ``scale_col``
+    [ceil(rows/128)][cols]), both from one read of x, or for 128 x 128 tiles
+    (``out_tile``, ``scale_tile``).  ``ldx`` is x's row stride (default cols;
+    x itself may be the view of a wider tensor's columns); see fp8lin.h."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"x: expected a torch.Tensor, got {type(x).__name__}")
+    if in_type is None:
+        in_type = _IN_OF_DTYPE.get(x.dtype)
+        if in_type is None:
+            raise ValueError(f"fp8_quantize_block: no input type for dtype {x.dtype}")
+    elif in_type not in (IN_BF16, IN_F16, IN_F32):
+        raise ValueError(f"fp8_quantize_block: bad input type {in_type}")
+    rows, cols = int(rows), int(cols)
+    if ldx is None:
+        ldx = cols
+    if rows < 0 or cols < 0 or ldx < cols:
+        raise ValueError(f"fp8_quantize_block: bad sizes {rows} x {cols}, ldx {ldx}")
+    if x.dtype not in (_F32 if in_type == IN_F32 else _BYTE2):
+        raise ValueError(f"x: dtype {x.dtype} for input type {in_type}")
+    if not x.is_contiguous() and not (x.dim() == 2 and x.stride(1) == 1 and x.stride(0) == ldx):
+        raise ValueError("x: must be contiguous, or 2-D with unit column stride and row stride "
+                         "ldx")
+    n = rows * cols
+    if n and _span(x) < (rows - 1) * ldx + cols:
+        raise ValueError(f"x: {_span(x)} elements, needs at least {(rows - 1) * ldx + cols}")
+    rg, cg = _groups(rows), _groups(cols)
+    if out_row is not None or scale_row is not None:
+        _buf(out_row, "out_row", n, _BYTE1, nullable=False)
+        _buf(scale_row, "scale_row", rows * cg, _F32, nullable=False)
+    if out_col is not None or scale_col is not None:
+        _buf(out_col, "out_col", n, _BYTE1, nullable=False)
+        _buf(scale_col, "scale_col", rg * cols, _F32, nullable=False)
+    if out_tile is not None or scale_tile is not None:
+        _buf(out_tile, "out_tile", n, _BYTE1, nullable=False)
+        _buf(scale_tile, "scale_tile", rg * cg, _F32, nullable=False)
+    st = _lib.fp8_quantize_block(_ptr(x), in_type, rows, cols, ldx, fmt, margin, _ptr(out_row),
+                                 _ptr(scale_row), _ptr(out_col), _ptr(scale_col),
+                                 _ptr(out_tile), _ptr(scale_tile), _stream(stream))
+    _check(st, "fp8_quantize_block")
+
+
+def _span(x: torch.Tensor) -> int:
+    """Elements from a tensor's first to its last, both counted."""
+    if x.is_contiguous():
+        return x.numel()
+    return (x.shape[0] - 1) * x.stride(0) + x.shape[1]
+
+
+def fp8_mm_block_workspace(m: int, n: int, k: int) -> int:
+    return int(_lib.fp8_mm_block_workspace(m, n, k))
+
+
+def fp8_mm_block(a: torch.Tensor, b: torch.Tensor, fmt_a: int, fmt_b: int, trans_a: int,
+                 trans_b: int, m: int, n: int, k: int, lda: int, ldb: int,
+                 scale_a: torch.Tensor, group_a: int, scale_b: torch.Tensor, group_b: int,
+                 bias: torch.Tensor | None, out: torch.Tensor,
+                 workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Product of operands with a step for each group of 128 k per row /
+    column (GROUP_LINE) or per 128 x 128 tile (GROUP_TILE); see fp8lin.h."""
+    m, n, k = int(m), int(n), int(k)
+    if m < 0 or n < 0 or k < 0:
+        raise ValueError("fp8_mm_block: negative size")
+    if group_a not in (GROUP_LINE, GROUP_TILE) or group_b not in (GROUP_LINE, GROUP_TILE):
+        raise ValueError(f"fp8_mm_block: bad grouping {group_a}, {group_b}")
+    kg = _groups(k)
+    _buf(a, "a", _extent(k, m, lda, 1, 0) if trans_a else _extent(m, k, lda, 1, 0), _BYTE1,
+         nullable=False)
+    _buf(b, "b", _extent(n, k, ldb, 1, 0) if trans_b else _extent(k, n, ldb, 1, 0), _BYTE1,
+         nullable=False)
+    _buf(scale_a, "scale_a", kg * (_groups(m) if group_a else m), _F32, nullable=False)
+    _buf(scale_b, "scale_b", kg * (_groups(n) if group_b else n), _F32, nullable=False)
+    _buf(bias, "bias", n, _BF16)
+    _buf(out, "out", m * n, _BF16, nullable=False)
+    st = _lib.fp8_mm_block(_ptr(a), _ptr(b), fmt_a, fmt_b, trans_a, trans_b, m, n, k, lda, ldb,
+                           _ptr(scale_a), group_a, _ptr(scale_b), group_b, _ptr(bias),
+                           _ptr(out), _ptr(workspace),
+                           0 if workspace is None else _ws_bytes(workspace, "workspace"),
+                           _stream(stream))
+    _check(st, "fp8_mm_block")
+
+
+def fp8_moe_workspace(tokens: int, experts: int, top_k: int, dim: int, hidden: int) -> int:
+    return int(_lib.fp8_moe_workspace(tokens, experts, top_k, dim, hidden))
+
+
+def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor,
+            w2: torch.Tensor, s2: torch.Tensor, tokens: int, experts: int, top_k: int, dim: int,
+            hidden: int, fmt: int, renormalize: bool, workspace: torch.Tensor,
+            out: torch.Tensor, ids: torch.Tensor | None = None,
+            weights: torch.Tensor | None = None, stream=None) -> None:
+    """A mixture-of-experts layer for a few tokens: router, top-k, gated
+    experts with tile-scaled fp8 weights, weighted sum; see fp8lin.h."""
+    if min(tokens, experts, top_k, dim, hidden) < 0:
+        raise ValueError("fp8_moe: negative size")
+    _buf(x, "x", tokens * dim, _BF16, nullable=False)
+    _buf(router, "router", experts * dim, _BF16, nullable=False)
+    _buf(w13, "w13", experts * 2 * hidden * dim, _BYTE1, nullable=False)
+    _buf(s13, "s13", experts * _groups(2 * hidden) * _groups(dim), _F32, nullable=False)
+    _buf(w2, "w2", experts * dim * hidden, _BYTE1, nullable=False)
+    _buf(s2, "s2", experts * _groups(dim) * _groups(hidden), _F32, nullable=False)
+    _buf(out, "out", tokens * dim, _BF16, nullable=False)
+    _buf(ids, "ids", tokens * top_k, (torch.int32,))
+    _buf(weights, "weights", tokens * top_k, _F32)
+    st = _lib.fp8_moe(_ptr(x), _ptr(router), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), tokens,
+                      experts, top_k, dim, hidden, fmt, int(bool(renormalize)), _ptr(workspace),
+                      _ws_bytes(workspace, "workspace"), _ptr(out), _ptr(ids), _ptr(weights),
+                      _stream(stream))
+    _check(st, "fp8_moe")

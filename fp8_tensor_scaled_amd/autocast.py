@@ -6,7 +6,8 @@ FP8TensorMeta, FP8State, fp8_autocast, fp8_linear_forward, _LinearFp8):
 
 * ``FP8Format``: E4M3, E5M2, or HYBRID (E4M3 forward, E5M2 gradients).
 * ``FP8Recipe``: delayed scaling over an amax history of ``history_len``
-  steps (the default), or dynamic (current-amax) scaling; ``margin`` divides
+  steps (the default), dynamic (current-amax) scaling, or block scaling (a
+  step from the current amax of each group of 128 values); ``margin`` divides
   the step by 2^margin.
 * ``fp8_autocast``: a context (a ContextVar, so threads and nested regions
   each see their own) that turns the fp8 path on for ``fp8_linear`` /
@@ -47,11 +48,12 @@ import weakref
 
 import torch
 
-from . import (E4M3, E5M2, OUT_BF16, Ring, _linear_bwd_call, _linear_fwd_call, _stream,
-               fp8_colsum, fp8_colsum_workspace,
+from . import (E4M3, E5M2, GROUP_LINE, GROUP_TILE, OUT_BF16, Ring, _groups, _linear_bwd_call,
+               _linear_fwd_call, _stream, fp8_colsum, fp8_colsum_workspace,
                fp8_linear_bwd, fp8_linear_bwd_workspace, fp8_linear_bwd_workspace_codes,
-               fp8_linear_fwd, fp8_linear_fwd_workspace, fp8_mm,
-               fp8_mm_ex, fp8_quantize, fp8_quantize_colsum)
+               fp8_linear_fwd, fp8_linear_fwd_workspace, fp8_mm, fp8_mm_block,
+               fp8_mm_block_workspace, fp8_mm_ex, fp8_quantize, fp8_quantize_block,
+               fp8_quantize_colsum)
 
 __all__ = ["FP8Format", "FP8Recipe", "FP8TensorMeta", "FP8State", "fp8_state", "fp8_autocast",
            "current_config", "fp8_linear", "FP8Linear", "fp8_linear_enable",
@@ -77,16 +79,22 @@ class FP8Format(str, enum.Enum):
 @dataclasses.dataclass(frozen=True)
 class FP8Recipe:
     """step = max(peak / FP8_MAX / 2^margin, 1e-12) with peak the max of the
-    amax history (delayed) or the current amax (dynamic)."""
+    amax history (delayed), the current amax (dynamic), or the current amax of
+    each block (block: activations and gradients in groups of 128 along the
+    product's contraction, weights in 128 x 128 tiles; no history)."""
     history_len: int = 16
     margin: int = 0
     dynamic: bool = False
+    block: bool = False
 
     def __post_init__(self):
         if not 1 <= self.history_len <= 4096:
             raise ValueError(f"history_len {self.history_len} outside [1, 4096]")
         if not 0 <= self.margin <= 64:
             raise ValueError(f"margin {self.margin} outside [0, 64]")
+        if self.block and self.dynamic:
+            raise ValueError("block scaling always takes the current amax: dynamic does not "
+                             "apply")
 
 
 @dataclasses.dataclass(frozen=True)
@@ -404,6 +412,102 @@ class _LinearFp8Weight(torch.autograd.Function):
         return dx, None, None, db, None, None
 
 
+@functools.lru_cache(maxsize=256)
+def _block_ws_size(m: int, n: int, k: int) -> int:
+    return fp8_mm_block_workspace(m, n, k)
+
+
+def _mm_block(a, b, fmt_a, fmt_b, trans_a, trans_b, m, n, k, sa, sb, group_b, bias, out) -> None:
+    """fp8_mm_block on dense operands, with the stream's workspace.  (Its
+    counters lie in the part that the linear calls keep at zero too.)"""
+    need = _block_ws_size(m, n, k)
+    fp8_mm_block(a, b, fmt_a, fmt_b, trans_a, trans_b, m, n, k, m if trans_a else k,
+                 k if trans_b else n, sa, GROUP_LINE, sb, group_b, bias, out,
+                 _workspace(a.device, need) if need else None)
+
+
+class _LinearFp8Block(torch.autograd.Function):
+    """y = x w^T + b and its gradients with block scaling: x and g have a
+    step for each row and group of 128 along the dimension that the product
+    sums over, the weight one for each 128 x 128 tile.
+
+        y  = x8 (groups along K) . w8^T
+        dX = g8 (groups along N) . w8          the forward's codes of w
+        dW = g8'^T . x8'                       groups along the rows, M
+
+    x's and g's second grouping comes from the same read as the first.  The
+    gradient's format may differ from that of x and w, which keep the
+    forward's.  A weight that arrives as codes with its tile steps is used as
+    it is and takes no gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w, w_scale, bias, cfg, grad_enabled):
+        N, K = w.shape
+        x2 = x.reshape(-1, K)
+        M = x2.shape[0]
+        dev = x.device
+        recipe, fmt = cfg.recipe, cfg.fp8_format.fwd()
+        need_x = grad_enabled and ctx.needs_input_grad[0]
+        need_w = grad_enabled and ctx.needs_input_grad[1]
+        ctx.margin, ctx.fmt, ctx.fmt_bwd = recipe.margin, fmt, cfg.fp8_format.bwd()
+        ctx.has_bias, ctx.x_shape, ctx.mnk = bias is not None, x.shape, (M, N, K)
+        u8, f32 = torch.uint8, torch.float32
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if w.dtype in _FP8_DTYPES:
+            w8, sw, ctx.fmt_w = w, w_scale, _FP8_DTYPES[w.dtype]
+        else:
+            ctx.fmt_w = fmt
+            w8 = torch.empty((N, K), dtype=u8, device=dev)
+            sw = torch.empty((_groups(N), _groups(K)), dtype=f32, device=dev)
+            fp8_quantize_block(w, N, K, fmt, out_tile=w8, scale_tile=sw, margin=recipe.margin)
+        x8c = sxc = None
+        if need_w:
+            x8c = torch.empty((M, K), dtype=u8, device=dev)
+            sxc = torch.empty((_groups(M), K), dtype=f32, device=dev)
+        if M > 0:
+            x8 = torch.empty((M, K), dtype=u8, device=dev)
+            sx = torch.empty((M, _groups(K)), dtype=f32, device=dev)
+            fp8_quantize_block(x2, M, K, fmt, out_row=x8, scale_row=sx, out_col=x8c,
+                               scale_col=sxc, margin=recipe.margin)
+            _mm_block(x8, w8, fmt, ctx.fmt_w, 0, 1, M, N, K, sx, sw, GROUP_TILE, bias, out)
+        ctx.save_for_backward(x8c, sxc, w8 if need_x else None, sw if need_x else None)
+        return out.reshape(*x.shape[:-1], N)
+
+    @staticmethod
+    def backward(ctx, g):
+        M, N, K = ctx.mnk
+        x8c, sxc, w8, sw = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad[:2]
+        need_b = ctx.has_bias and ctx.needs_input_grad[3]
+        dev, u8, f32, b16 = g.device, torch.uint8, torch.float32, torch.bfloat16
+        make = torch.zeros if M == 0 else torch.empty
+        dx = make((M, K), dtype=b16, device=dev) if need_x else None
+        dw = make((N, K), dtype=b16, device=dev) if need_w else None
+        db = make(N, dtype=b16, device=dev) if need_b else None
+        if M > 0:
+            g2 = _bf16(g.reshape(-1, N), "the output gradient")
+            g8 = sg = g8c = sgc = None
+            if need_x:
+                g8 = torch.empty((M, N), dtype=u8, device=dev)
+                sg = torch.empty((M, _groups(N)), dtype=f32, device=dev)
+            if need_w:
+                g8c = torch.empty((M, N), dtype=u8, device=dev)
+                sgc = torch.empty((_groups(M), N), dtype=f32, device=dev)
+            if need_x or need_w:
+                fp8_quantize_block(g2, M, N, ctx.fmt_bwd, out_row=g8, scale_row=sg,
+                                   out_col=g8c, scale_col=sgc, margin=ctx.margin)
+            if need_x:
+                _mm_block(g8, w8, ctx.fmt_bwd, ctx.fmt_w, 0, 0, M, K, N, sg, sw, GROUP_TILE,
+                          None, dx)
+            if need_w:
+                _mm_block(g8c, x8c, ctx.fmt_bwd, ctx.fmt, 1, 0, N, K, M, sgc, sxc, GROUP_LINE,
+                          None, dw)
+            if need_b:
+                ws = torch.empty(fp8_colsum_workspace(M, N), dtype=u8, device=dev)
+                fp8_colsum(g2, M, N, db, ws)
+        return (None if dx is None else dx.reshape(ctx.x_shape), dw, None, db, None, None)
+
+
 def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
                w_scale: torch.Tensor | None = None,
                b_scale: torch.Tensor | None = None) -> torch.Tensor:
@@ -411,7 +515,9 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     default switch) enables it.  w: bf16 [N][K], or fp8 codes [N][K] with
     their step ``w_scale`` (fp32 [1], device).  With fp8 weight codes the
     bias may be fp8 codes [N] of the same format with their step
-    ``b_scale`` ([LOG1] bias_scale), dequantized in the GEMM's epilogue."""
+    ``b_scale`` ([LOG1] bias_scale), dequantized in the GEMM's epilogue.
+    Under a block recipe fp8 weight codes come with the steps of their
+    128 x 128 tiles (fp32 [ceil(N/128)][ceil(K/128)])."""
     cfg = current_config()
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"fp8_linear: input of shape {tuple(x.shape)} and weight of shape "
@@ -427,10 +533,22 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
             raise ValueError("fp8_linear: a pre-quantized weight needs w_scale")
         if not cfg.enabled:
             raise ValueError("fp8_linear: a pre-quantized weight needs the fp8 path enabled")
+        if cfg.recipe.block:
+            if bias8:
+                raise ValueError("fp8_linear: block scaling takes a bf16 bias")
+            tiles = (_groups(w.shape[0]), _groups(w.shape[1]))
+            if tuple(w_scale.shape) != tiles:
+                raise ValueError(f"fp8_linear: w_scale of shape {tuple(w_scale.shape)}, expected "
+                                 f"{tiles} (a step for each 128 x 128 tile)")
+            return _LinearFp8Block.apply(_bf16(x, "x"), w.contiguous(), w_scale.contiguous(),
+                                         _bf16(bias, "bias"), cfg, torch.is_grad_enabled())
         return _LinearFp8Weight.apply(_bf16(x, "x"), w, w_scale,
                                       bias if bias8 else _bf16(bias, "bias"), b_scale, cfg)
     if not cfg.enabled:
         return torch.nn.functional.linear(x, w, bias)
+    if cfg.recipe.block:
+        return _LinearFp8Block.apply(_bf16(x, "x"), _bf16(w, "w"), None, _bf16(bias, "bias"), cfg,
+                                     torch.is_grad_enabled())
     return _LinearFp8.apply(_bf16(x, "x"), _bf16(w, "w"), _bf16(bias, "bias"), cfg,
                             torch.is_grad_enabled())
 

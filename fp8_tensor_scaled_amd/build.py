@@ -14,7 +14,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8lin.so")
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_tiled.hip", "gemm_skinny.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_tiled.hip", "gemm_skinny.hip",
+           "block_api.hip", "block_quant.hip", "block_gemm.hip", "moe.hip"]
 # the benchmark's ceiling kernels, a library of their own that only bench.py loads
 BENCH_LIB = os.path.join(HERE, "libfp8bench.so")
 BENCH_SOURCES = ["bench_ref.hip"]

@@ -19,11 +19,16 @@
 #include <string.h>
 
 #include "../../include/fp8lin.h"
+#include "api_util.hpp"
 #include "internal.hpp"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
+
+namespace fp8lin {
+
+void clear_error() { g_err[0] = 0; }
 
 fp8_status_t fail(fp8_status_t st, const char* fmt, ...) {
     va_list ap;
@@ -57,7 +62,14 @@ fp8_status_t check_device() {
     return FP8_OK;
 }
 
-bool fmt_ok(fp8_fmt_t f) { return f == FP8_E4M3 || f == FP8_E5M2; }
+}  // namespace fp8lin
+
+namespace {
+
+using fp8lin::check_device;
+using fp8lin::fail;
+using fp8lin::fmt_ok;
+using fp8lin::hip_fail;
 
 fp8_status_t check_ring(const fp8_ring_t* r, const char* name) {
     if (!r) return fail(FP8_EINVAL, "%s: ring is NULL", name);

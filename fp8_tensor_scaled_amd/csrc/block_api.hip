@@ -1,0 +1,232 @@
+// C entry points of the block-scaled operators: argument validation and the
+// hand-over to the launches.  Declarations and contracts: fp8lin.h.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+
+#include "../../include/fp8lin.h"
+#include "api_util.hpp"
+#include "block.hpp"
+
+using fp8lin::check_device;
+using fp8lin::clear_error;
+using fp8lin::fail;
+using fp8lin::fmt_ok;
+using fp8lin::groups_of;
+using fp8lin::hip_fail;
+
+extern "C" {
+
+fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols,
+                                int64_t ldx, fp8_fmt_t fmt, int32_t margin, uint8_t* out_row,
+                                float* scale_row, uint8_t* out_col, float* scale_col,
+                                uint8_t* out_tile, float* scale_tile, hipStream_t stream) {
+    clear_error();
+    const char* who = "fp8_quantize_block";
+    if (!fmt_ok(fmt)) return fail(FP8_EINVAL, "%s: unsupported fp8 format %d", who, fmt);
+    if (in_type != FP8_IN_BF16 && in_type != FP8_IN_F16 && in_type != FP8_IN_F32)
+        return fail(FP8_EINVAL, "%s: unsupported input type %d", who, (int)in_type);
+    if (rows < 0 || cols < 0)
+        return fail(FP8_EINVAL, "%s: rows, cols must be >= 0 (got %lld, %lld)", who,
+                    (long long)rows, (long long)cols);
+    if (ldx < cols)
+        return fail(FP8_EINVAL, "%s: ldx %lld < cols %lld", who, (long long)ldx,
+                    (long long)cols);
+    if ((double)rows * (double)ldx >= 9.0e15)
+        return fail(FP8_EINVAL, "%s: too many elements", who);
+    if (margin < 0 || margin > 64)
+        return fail(FP8_EINVAL, "%s: margin %d outside [0, 64]", who, margin);
+    if (rows == 0 || cols == 0) return FP8_OK;  // (empty tensors may have no address)
+    if ((out_row == nullptr) != (scale_row == nullptr) ||
+        (out_col == nullptr) != (scale_col == nullptr) ||
+        (out_tile == nullptr) != (scale_tile == nullptr))
+        return fail(FP8_EINVAL, "%s: codes and steps of a grouping go together", who);
+    if (!out_row && !out_col && !out_tile) return fail(FP8_EINVAL, "%s: no output given", who);
+    if (out_tile && (out_row || out_col))
+        return fail(FP8_EINVAL, "%s: tiles go alone (rows and columns may go together)", who);
+    if (!x) return fail(FP8_EINVAL, "%s: x is NULL", who);
+    if ((uintptr_t)x % (in_type == FP8_IN_F32 ? 4 : 2))
+        return fail(FP8_EINVAL, "%s: x is not aligned to its elements", who);
+    if ((double)groups_of(rows) * (double)groups_of(cols) >= 2147483647.0)
+        return fail(FP8_EINVAL, "%s: too many blocks", who);
+    if (out_row && out_col) {
+        const uintptr_t a = (uintptr_t)out_row, b = (uintptr_t)out_col;
+        const uintptr_t n = (uintptr_t)(rows * cols);
+        if (a < b + n && b < a + n)
+            return fail(FP8_EINVAL, "%s: out_row and out_col overlap", who);
+    }
+    fp8_status_t st = check_device();
+    if (st) return st;
+    fp8lin::BlockQuantLaunch q;
+    q.x = x;
+    q.in_type = in_type;
+    q.rows = rows;
+    q.cols = cols;
+    q.ldx = ldx;
+    q.fmt = fmt;
+    q.rmargin = ldexpf(1.0f, -margin);
+    q.out_row = out_row;
+    q.scale_row = scale_row;
+    q.out_col = out_col;
+    q.scale_col = scale_col;
+    q.out_tile = out_tile;
+    q.scale_tile = scale_tile;
+    hipError_t e = fp8lin::launch_quantize_block(q, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "block quantize launch");
+}
+
+size_t fp8_mm_block_workspace(int64_t m, int64_t n, int64_t k) {
+    if (m < 1 || n < 1 || k < 1) return 0;
+    return fp8lin::block_gemm_workspace(m, n, k);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Where a step lies (BlockScale) for an operand whose rows (of A, columns of
+// B) number `lines`, stored with the lines contiguous along k or across it.
+fp8lin::BlockScale scale_of(const float* s, fp8_group_t group, bool k_major, int64_t lines,
+                            int64_t k) {
+    fp8lin::BlockScale r;
+    r.s = s;
+    r.shift = group == FP8_GROUP_TILE ? 7 : 0;
+    const int64_t along = group == FP8_GROUP_TILE ? groups_of(lines) : lines;
+    r.si = k_major ? groups_of(k) : 1;
+    r.sk = k_major ? 1 : along;
+    return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, fp8_fmt_t fmt_b,
+                          int32_t trans_a, int32_t trans_b, int64_t m, int64_t n, int64_t k,
+                          int64_t lda, int64_t ldb, const float* scale_a, fp8_group_t group_a,
+                          const float* scale_b, fp8_group_t group_b, const uint16_t* bias,
+                          uint16_t* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+    clear_error();
+    const char* who = "fp8_mm_block";
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b))
+        return fail(FP8_EINVAL, "%s: unsupported fp8 format %d, %d", who, fmt_a, fmt_b);
+    if (!a || !b || !out || !scale_a || !scale_b)
+        return fail(FP8_EINVAL, "%s: NULL operand, output or scale", who);
+    if ((trans_a != 0 && trans_a != 1) || (trans_b != 0 && trans_b != 1))
+        return fail(FP8_EINVAL, "%s: trans flags must be 0 or 1", who);
+    if ((group_a != FP8_GROUP_LINE && group_a != FP8_GROUP_TILE) ||
+        (group_b != FP8_GROUP_LINE && group_b != FP8_GROUP_TILE))
+        return fail(FP8_EINVAL, "%s: unsupported grouping %d, %d", who, (int)group_a,
+                    (int)group_b);
+    if (m < 1 || n < 1 || k < 1)
+        return fail(FP8_EINVAL, "%s: m, n, k must be >= 1 (got %lld, %lld, %lld)", who,
+                    (long long)m, (long long)n, (long long)k);
+    const int64_t a_cols = trans_a ? m : k, b_cols = trans_b ? k : n;
+    if (lda < a_cols)
+        return fail(FP8_EINVAL, "%s: lda %lld < %lld", who, (long long)lda, (long long)a_cols);
+    if (ldb < b_cols)
+        return fail(FP8_EINVAL, "%s: ldb %lld < %lld", who, (long long)ldb, (long long)b_cols);
+    if ((double)m * (double)n >= 1099511627776.0 ||
+        (double)(trans_a ? k : m) * (double)lda >= 9.0e15 ||
+        (double)(trans_b ? n : k) * (double)ldb >= 9.0e15)
+        return fail(FP8_EINVAL, "%s: operand or output too large", who);
+    if (((uintptr_t)out | (uintptr_t)bias) & 1)
+        return fail(FP8_EINVAL, "%s: out or bias is not aligned to its elements", who);
+    if (((uintptr_t)scale_a | (uintptr_t)scale_b) & 3)
+        return fail(FP8_EINVAL, "%s: a scale is not aligned to its elements", who);
+    const size_t need = fp8lin::block_gemm_workspace(m, n, k);
+    if (workspace) {
+        if (workspace_bytes < need)
+            return fail(FP8_EINVAL, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
+        if ((uintptr_t)workspace & 255)
+            return fail(FP8_EINVAL, "%s: workspace not 256-byte aligned", who);
+    }
+    fp8_status_t st = check_device();
+    if (st) return st;
+    fp8lin::BlockGemmLaunch g;
+    g.a = a;
+    g.b = b;
+    g.fmt_a = fmt_a;
+    g.fmt_b = fmt_b;
+    g.trans_a = trans_a;
+    g.trans_b = trans_b;
+    g.m = m;
+    g.n = n;
+    g.k = k;
+    g.lda = lda;
+    g.ldb = ldb;
+    g.sa = scale_of(scale_a, group_a, trans_a == 0, m, k);
+    g.sb = scale_of(scale_b, group_b, trans_b != 0, n, k);
+    g.bias = bias;
+    g.out = out;
+    g.ws = need ? workspace : nullptr;
+    hipError_t e = fp8lin::launch_block_gemm(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "block gemm launch");
+}
+
+static const char* moe_sizes_error(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim,
+                                   int64_t hidden) {
+    if (tokens < 0 || tokens > 1024) return "tokens outside [0, 1024]";
+    if (experts < 1 || experts > 512) return "experts outside [1, 512]";
+    if (top_k < 1 || top_k > 16 || top_k > experts) return "top_k outside [1, min(16, experts)]";
+    if (dim < 16 || dim > 65536 || dim % 16) return "dim must be a multiple of 16 up to 65536";
+    if (hidden < 16 || hidden > 65536 || hidden % 16)
+        return "hidden must be a multiple of 16 up to 65536";
+    return nullptr;
+}
+
+size_t fp8_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim,
+                         int64_t hidden) {
+    if (moe_sizes_error(tokens, experts, top_k, dim, hidden)) return 0;
+    return fp8lin::moe_workspace(tokens, experts, top_k, dim, hidden);
+}
+
+fp8_status_t fp8_moe(const uint16_t* x, const uint16_t* router, const uint8_t* w13,
+                     const float* s13, const uint8_t* w2, const float* s2, int64_t tokens,
+                     int64_t experts, int64_t top_k, int64_t dim, int64_t hidden, fp8_fmt_t fmt,
+                     int32_t renormalize, void* workspace, size_t workspace_bytes, uint16_t* out,
+                     int32_t* ids, float* weights, hipStream_t stream) {
+    clear_error();
+    const char* who = "fp8_moe";
+    if (!fmt_ok(fmt)) return fail(FP8_EINVAL, "%s: unsupported fp8 format %d", who, fmt);
+    if (const char* why = moe_sizes_error(tokens, experts, top_k, dim, hidden))
+        return fail(FP8_EINVAL, "%s: %s", who, why);
+    if (tokens == 0) return FP8_OK;
+    if (!x || !router || !w13 || !s13 || !w2 || !s2 || !workspace || !out)
+        return fail(FP8_EINVAL, "%s: NULL operand, workspace or output", who);
+    if (((uintptr_t)x | (uintptr_t)router | (uintptr_t)w13 | (uintptr_t)w2 | (uintptr_t)out) & 15)
+        return fail(FP8_EINVAL, "%s: x, router, weights and out must be 16-byte aligned", who);
+    if (((uintptr_t)s13 | (uintptr_t)s2 | (uintptr_t)ids | (uintptr_t)weights) & 3)
+        return fail(FP8_EINVAL, "%s: steps, ids or weights not aligned to their elements", who);
+    const size_t need = fp8lin::moe_workspace(tokens, experts, top_k, dim, hidden);
+    if (workspace_bytes < need)
+        return fail(FP8_EINVAL, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
+    if ((uintptr_t)workspace & 255)
+        return fail(FP8_EINVAL, "%s: workspace not 256-byte aligned", who);
+    fp8_status_t st = check_device();
+    if (st) return st;
+    fp8lin::MoeLaunch g;
+    g.x = x;
+    g.router = router;
+    g.w13 = w13;
+    g.s13 = s13;
+    g.w2 = w2;
+    g.s2 = s2;
+    g.tokens = (int)tokens;
+    g.experts = (int)experts;
+    g.top_k = (int)top_k;
+    g.dim = (int)dim;
+    g.hidden = (int)hidden;
+    g.fmt = fmt;
+    g.renorm = renormalize != 0;
+    g.ws = workspace;
+    g.out = out;
+    g.ids = ids;
+    g.weights = weights;
+    hipError_t e = fp8lin::launch_moe(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "mixture-of-experts launch");
+}
+
+}  // extern "C"

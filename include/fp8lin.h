@@ -460,6 +460,106 @@ fp8_status_t fp8_linear_bwd(const uint16_t* g, const uint16_t* x, const uint16_t
                             float* scales_out, uint16_t* dx, uint16_t* dw, uint16_t* db,
                             const uint8_t* x8_bwd, const uint8_t* w8_bwd, hipStream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Block scaling: one step for each group of 128 values instead of one per
+ * tensor.  A matrix is grouped along its rows (1 x 128, the last group of a
+ * row may be shorter), along its columns (128 x 1) or in 128 x 128 tiles.
+ * ------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------
+ * fp8_quantize_block -- bf16 / fp16 / fp32 -> fp8 codes, a step per group.
+ *
+ *   s[group] = max( fp32( max |x| * fp32(1 / FMAX) ) * 2^-margin , 1e-12 )
+ *   out      = encode_fmt( fp32( x * fp32(1 / s) ) )
+ *
+ * with fp8_quantize's encode (nearest even, saturating, NaN stays NaN) and
+ * NaN skipped in the maxima.  A group that holds an infinity has an infinite
+ * step: its infinities become NaN codes and its other values 0, so that
+ * code * step is NaN throughout.
+ *
+ * x: [rows][cols] of type in_type, row stride ldx >= cols elements, any
+ *    alignment of whole elements.  rows, cols >= 0 (0: nothing is written).
+ * out_row, scale_row:   codes [rows][cols], steps [rows][ceil(cols / 128)].
+ * out_col, scale_col:   codes [rows][cols], steps [ceil(rows / 128)][cols].
+ * out_tile, scale_tile: codes [rows][cols], steps
+ *    [ceil(rows / 128)][ceil(cols / 128)].
+ * Codes and steps of a grouping are both given or both NULL.  Row and column
+ * groupings may be asked together (one read of x; they must not overlap),
+ * tiles alone.  All outputs are contiguous.  margin: 0 .. 64.
+ * ------------------------------------------------------------------- */
+fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, int64_t cols,
+                                int64_t ldx, fp8_fmt_t fmt, int32_t margin, uint8_t* out_row,
+                                float* scale_row, uint8_t* out_col, float* scale_col,
+                                uint8_t* out_tile, float* scale_tile, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_mm_block -- product of block-scaled operands.
+ *
+ *   out[i][j] = bf16_rne( sum_kb sa(i,kb) sb(kb,j) sum_{k in kb} A[i][k] B[k][j] + bias[j] )
+ *
+ * with kb the groups of 128 k and fp32 sums.
+ * a, b, trans_a, trans_b, m, n, k, lda, ldb: storage as fp8_mm (one batch).
+ * fmt_a, fmt_b: the operands' formats, which may differ (an E5M2 gradient
+ *     times an E4M3 weight).
+ * group_a: FP8_GROUP_LINE -- a step for each row of A and group of k: the
+ *     row grouping of a [m][k] matrix (trans_a 0, steps [m][ceil(k/128)]) or
+ *     the column grouping of a [k][m] one (trans_a 1, [ceil(k/128)][m]);
+ *     FP8_GROUP_TILE -- a step for each 128 x 128 tile of the stored matrix.
+ * group_b: the same for B's columns: FP8_GROUP_LINE is the row grouping of a
+ *     [n][k] matrix (trans_b 1) or the column grouping of a [k][n] one.
+ * bias: bf16 [n] or NULL.  out: bf16 [m][n], contiguous.
+ * workspace: NULL, or device scratch of fp8_mm_block_workspace(m, n, k)
+ *     bytes (may be 0), 256-byte aligned, zero before its first use and
+ *     left so that it can be reused: with it a product of few outputs and
+ *     long k is split along k over more workgroups.  The sums are added in a
+ *     fixed order, so a call's result does not vary from run to run.
+ * ------------------------------------------------------------------- */
+typedef enum { FP8_GROUP_LINE = 0, FP8_GROUP_TILE = 1 } fp8_group_t;
+
+size_t fp8_mm_block_workspace(int64_t m, int64_t n, int64_t k);
+fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, fp8_fmt_t fmt_b,
+                          int32_t trans_a, int32_t trans_b, int64_t m, int64_t n, int64_t k,
+                          int64_t lda, int64_t ldb, const float* scale_a, fp8_group_t group_a,
+                          const float* scale_b, fp8_group_t group_b, const uint16_t* bias,
+                          uint16_t* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * fp8_moe -- a whole mixture-of-experts layer for a few tokens.
+ *
+ *   l = x R^T (fp32);  e_1 .. e_k = the top_k largest of l, ties to the
+ *   lowest index;  w_j = softmax(l)[e_j], divided by their sum when
+ *   renormalize != 0;
+ *   out = bf16_rne( sum_j w_j W2[e_j] ( silu(G[e_j] x) * (U[e_j] x) ) )
+ *
+ * A weight is its code times the step of its 128 x 128 tile; activations
+ * keep bf16 or more between the products, sums are fp32.
+ * x: bf16 [tokens][dim].  router: bf16 [experts][dim].
+ * w13: codes [experts][2 * hidden][dim], G's rows and then U's; s13: steps
+ *     [experts][ceil(2 * hidden / 128)][ceil(dim / 128)].
+ * w2: codes [experts][dim][hidden]; s2: steps
+ *     [experts][ceil(dim / 128)][ceil(hidden / 128)].
+ * 0 <= tokens <= 1024 (0: nothing happens), 1 <= experts <= 512,
+ * 1 <= top_k <= min(16, experts); dim and hidden multiples of 16 up to
+ * 65536; x, router, w13, w2 and out 16-byte aligned.  The work is shaped for
+ * the reading of the chosen experts' weights, which bounds it up to a few
+ * tokens per expert; more tokens are computed rightly, not at a large
+ * product's rate.
+ * A logit that is NaN ranks below every number; such a token's weights, and
+ * its outputs, are NaN.
+ * workspace: fp8_moe_workspace(...) bytes of device scratch, 256-byte
+ *     aligned, zero before its first use and left so that it can be reused.
+ * ids, weights: nullable, [tokens][top_k]: e_j (int32) and w_j (fp32),
+ *     largest first.
+ * ------------------------------------------------------------------- */
+size_t fp8_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim,
+                         int64_t hidden);
+fp8_status_t fp8_moe(const uint16_t* x, const uint16_t* router, const uint8_t* w13,
+                     const float* s13, const uint8_t* w2, const float* s2, int64_t tokens,
+                     int64_t experts, int64_t top_k, int64_t dim, int64_t hidden, fp8_fmt_t fmt,
+                     int32_t renormalize, void* workspace, size_t workspace_bytes, uint16_t* out,
+                     int32_t* ids, float* weights, hipStream_t stream);
+
 /* Message of the last non-OK status returned on the calling thread
  * (thread-local; "" if none). */
 const char* fp8_last_error(void);
