@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8lin.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_tiled.hip", "gemm_skinny.hip",
-           "block_api.hip", "block_quant.hip", "block_gemm.hip", "moe.hip"]
+           "block_api.hip", "block_quant.hip", "block_gemm.hip",
+           "block_gemm_nt.hip", "block_gemm_nn.hip", "block_gemm_tn.hip", "moe.hip"]
 # the benchmark's ceiling kernels, a library of their own that only bench.py loads
 BENCH_LIB = os.path.join(HERE, "libfp8bench.so")
 BENCH_SOURCES = ["bench_ref.hip"]
@@ -64,7 +65,7 @@ def build(verbose: bool = False) -> str:
             print(msgs, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(6, len(SOURCES) + len(BENCH_SOURCES))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + len(BENCH_SOURCES))) as ex:
         objs = list(ex.map(compile_one, SOURCES + BENCH_SOURCES))
     for lib, parts in ((LIB, objs[:len(SOURCES)]), (BENCH_LIB, objs[len(SOURCES):])):
         tmp = lib + ".tmp%d" % os.getpid()

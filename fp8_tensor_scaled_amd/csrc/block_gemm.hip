@@ -5,12 +5,14 @@
 // product of the two steps and added to the running sum (one rounding of
 // the product of the steps, one fused multiply-add per group).
 //
-// This file holds the dispatcher and the general kernel, which takes any
+// This file holds the dispatcher and the general kernel (the tiled kernels
+// are block_gemm_tile.hpp's), which takes any
 // layout, size, stride and alignment: every lane gathers its operand bytes
 // one by one and each wave owns a 16 x 16 output tile, whose 16x16x128
 // matrix instruction covers exactly one group of k.
 
 #include "block.hpp"
+#include "block_gemm_tile.hpp"
 #include "common.hpp"
 
 namespace fp8lin {
@@ -82,7 +84,38 @@ hipError_t launch_general(const BlockGemmLaunch& g, hipStream_t stream) {
 
 size_t block_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
 
+// What the tiled kernels take: 16-byte aligned operands and leading
+// dimensions, whole 16-byte pieces along the contiguous dimension, operands
+// that 32-bit offsets reach.
+static bool tiled_supported(const BlockGemmLaunch& g) {
+    if (g.fmt_a == 0 && g.fmt_b == 1) return false;
+    if (g.trans_a && g.trans_b) return false;
+    if ((reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.b)) & 15) return false;
+    if (g.lda % 16 || g.ldb % 16) return false;
+    if ((g.trans_a ? g.m : g.k) % 16 || (g.trans_b ? g.k : g.n) % 16) return false;
+    const double lim = 2147483647.0;
+    if ((double)(g.trans_a ? g.k : g.m) * (double)g.lda >= lim) return false;
+    if ((double)(g.trans_b ? g.n : g.k) * (double)g.ldb >= lim) return false;
+    if ((double)g.sa.sk >= lim / 4 || (double)g.sb.sk >= lim / 4) return false;
+    return (double)((g.m + 127) / 128) * (double)((g.n + 127) / 128) < lim;
+}
+
+static BlockCfg tile_cfg(const BlockGemmLaunch& g) {
+    auto rounds = [&](int bm, int bn) {
+        return (((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn) + 255) / 256;
+    };
+    const BlockCfg half = g.n >= g.m ? BlockCfg::kWide : BlockCfg::kTall;
+    const int64_t half_rounds = g.n >= g.m ? rounds(128, 256) : rounds(256, 128);
+    return half_rounds * 675 <= rounds(128, 128) * 475 ? half : BlockCfg::kMid;
+}
+
 hipError_t launch_block_gemm(const BlockGemmLaunch& g, hipStream_t stream) {
+    if (tiled_supported(g)) {
+        const bool bvec = g.sb.shift == 0;
+        const BlockCfg c = tile_cfg(g);
+        if (g.trans_a) return launch_block_tn(g, bvec, c, stream);
+        return g.trans_b ? launch_block_nt(g, bvec, c, stream) : launch_block_nn(g, bvec, c, stream);
+    }
     if (g.fmt_a == 0) return g.fmt_b == 0 ? launch_general<0, 0>(g, stream)
                                           : launch_general<0, 1>(g, stream);
     return g.fmt_b == 0 ? launch_general<1, 0>(g, stream) : launch_general<1, 1>(g, stream);

@@ -1,0 +1,416 @@
+// LDS-tiled block-scaled fp8 GEMM: the kernel template.  The instances are
+// compiled per storage layout (block_gemm_{nt,nn,tn}.hip).
+//
+//   out[i][j] = bf16( sum_kb sa(i,kb) sb(kb,j) P_kb[i][j] + bias[j] ),
+//   P_kb[i][j] = sum over the 128 k of group kb of A[i][k] B[k][j].
+//
+// The tiles, the ring of LDS stages and the operand layouts are the
+// per-tensor kernel's (gemm_operand.hpp).  What is different:
+//
+//  * A stage holds 128 k: exactly one group.  Its two 64-k matrix
+//    instructions start from zero and chain, so a 32 x 32 tile's P_kb is in 16
+//    registers after them, and 16 fused multiply-adds put it, times the
+//    steps, into the running sum.  Those take half the vector unit's time
+//    that the two matrix instructions take of the matrix unit's, and run in
+//    the shadow of the next tile's (the order below: in the second substep,
+//    tile t - 1's sums follow tile t's matrix instruction; the last tile's
+//    follow the next stage's first).
+//  * The matrix instruction takes the B fragment first, so a lane's 16
+//    values of a tile belong to one row of A: with one step per 128 x 128
+//    tile of B the factor is one number per lane and tile.  With a step per
+//    column (BVEC) each value has a factor of its own: twice the vector work.
+//  * The steps of a stage come with its operands, one load into LDS per
+//    wave: entry e < BM is row e's step, the others B's columns' (or its
+//    tiles').  Read by gathers in every wave they would be fetched WN
+//    times, from 32 lines each time.
+
+#pragma once
+
+#include <type_traits>
+
+#include "block.hpp"
+#include "gemm_operand.hpp"
+
+namespace fp8lin {
+
+struct BlockTileParams {
+    const uint8_t* a;
+    const uint8_t* b;
+    BlockScale sa, sb;
+    const uint16_t* bias;
+    uint16_t* out;
+    int64_t m, n, k, lda, ldb;
+    int tiles_m, tiles_n, group_m;
+    int vec_out16;  // whole 16-byte chunks of output rows (and bias), aligned
+    int xcd_remap;
+};
+
+// One global -> LDS load of a dword per lane: lane l's goes to LDS at M0 + 4 l.
+// No output register (see dma16).
+__device__ __forceinline__ void dma4(uint64_t addr, uint32_t lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(addr), "{m0}"(lds));
+}
+
+template <int FA, int FB>
+__device__ __forceinline__ v16f mfma_ba(const v8i& b, const v8i& a, v16f acc) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, FB, FA, 0, 0, 0, 0);
+}
+
+template <bool BVEC, int BM, int BN, int WM, int WN, int ST>
+struct BlockTile {
+    static constexpr int NW = WM * WN;
+    static constexpr int kStage = (BM + BN) * kGroup;  // operand bytes of a stage
+    static constexpr int kNB = BVEC ? BN : (BN + kGroup - 1) / kGroup;  // B's steps
+    static constexpr int kPer = (BM + kNB + NW - 1) / NW;  // steps each wave loads
+    static_assert(kPer <= 64, "one step per lane");
+    static constexpr int kSteps = (kPer * NW + 31) / 32 * 32;  // floats per stage
+    static constexpr int kLds = ST * (kStage + 4 * kSteps);
+    static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTileParams p) {
+    using BT = BlockTile<BVEC, BM, BN, WM, WN, ST>;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[BT::kLds];
+    constexpr int NW = BT::NW, BK = kGroup, kStage = BT::kStage, kPer = BT::kPer;
+    constexpr int kStageA = BM * BK;
+    constexpr int TM = BM / WM, TN = BN / WN;
+    constexpr int FM = TM / 32, FN = TN / 32, kMF = FM * FN;
+    static_assert(TN <= kGroup && kGroup % TN == 0, "a wave's columns share a tile of B");
+    using OA = Operand<AMN, BM, NW, BK>;
+    using OB = Operand<BMN, BN, NW, BK>;
+    constexpr int kPA = OA::kPerWave, kPB = OB::kPerWave;
+    constexpr int kLoads = kPA + kPB + 1;  // loads per wave and stage, the steps' last
+    static_assert(ST >= 2 && kLoads * (ST - 1) < 64, "vmcnt range");
+    uint8_t* steps = smem + ST * kStage;
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+
+    int bid = blockIdx.x;
+    if (p.xcd_remap) bid = (bid & 7) * ((int)gridDim.x >> 3) + (bid >> 3);
+    const int per_group = p.group_m * p.tiles_n;
+    const int first_m = (bid / per_group) * p.group_m;
+    const int gsz = p.tiles_m - first_m < p.group_m ? p.tiles_m - first_m : p.group_m;
+    const int r = bid - (bid / per_group) * per_group;
+    const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane((first_m + r % gsz) * BM);
+    const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane((r / gsz) * BN);
+
+    const v4i ra = make_rsrc(p.a + (AMN ? m0 : m0 * p.lda));
+    const v4i rb = make_rsrc(p.b + (BMN ? n0 : n0 * p.ldb));
+    const uint32_t lda = (uint32_t)p.lda, ldb = (uint32_t)p.ldb;
+    const int kdim = (int)p.k;
+    const int nk = (kdim + BK - 1) / BK;
+    const int64_t arows = p.m - m0, brows = p.n - n0;
+    const bool afull = arows >= BM, bfull = brows >= BN;
+    const uint32_t abase = OA::init(lda, arows, wave, lane);
+    const uint32_t bbase = OB::init(ldb, brows, wave, lane);
+
+    // This lane's step: its address at group 0 and the bytes to the next
+    // group.  Rows (columns) past the matrix read its last one's.
+    uint64_t step_at;
+    uint32_t step_k;
+    {
+        int e = wave * kPer + (lane < kPer ? lane : kPer - 1);
+        if (e >= BM + BT::kNB) e = BM + BT::kNB - 1;
+        const bool is_b = e >= BM;
+        int64_t i;
+        if (!is_b) {
+            i = m0 + e < p.m ? m0 + e : p.m - 1;
+        } else {
+            const int64_t j = BVEC ? n0 + (e - BM) : (n0 / kGroup + (e - BM)) * kGroup;
+            i = j < p.n ? j : p.n - 1;
+        }
+        const BlockScale& s = is_b ? p.sb : p.sa;
+        step_at = reinterpret_cast<uint64_t>(s.s + (i >> s.shift) * s.si);
+        step_k = (uint32_t)(s.sk * 4);
+    }
+
+    // Load x of the stage at group kg into ring slot s.
+    auto load = [&](int x, int s, int kg) __attribute__((always_inline)) {
+        uint8_t* dst = smem + s * kStage;
+        if (x < kPA) {
+            dma16(ra, OA::lds_of(dst, x, wave),
+                  OA::off_of(abase, lda, kg * BK, kdim, afull, arows, x, wave, lane));
+        } else if (x < kPA + kPB) {
+            dma16(rb, OB::lds_of(dst + kStageA, x - kPA, wave),
+                  OB::off_of(bbase, ldb, kg * BK, kdim, bfull, brows, x - kPA, wave, lane));
+        } else {
+            const int g = kg < nk ? kg : nk - 1;  // past the end: any group
+            if (lane < kPer)
+                dma4(step_at + (uint64_t)g * step_k,
+                     lds_addr(steps + 4 * (s * BT::kSteps + wave * kPer)));
+        }
+    };
+
+    v8i af[2][FM], bf[2][FN];
+    uint32_t aoff[FM], boff[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) aoff[i] = OA::frag_off(AMN ? wm * TM + 32 * i : 0, lane);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) boff[j] = OB::frag_off(BMN ? wn * TN + 32 * j : 0, lane);
+    constexpr int kRowA = AMN ? 0 : BK, kRowB = BMN ? 0 : BK;
+    const uint32_t arow = (uint32_t)(wm * TM * kRowA), brow = (uint32_t)(wn * TN * kRowB);
+
+    auto barrier = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+
+    v16f acc[FM][FN], part[kMF];
+#pragma unroll
+    for (int t = 0; t < kMF; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[t % FM][t / FM][e] = 0.0f, part[t][e] = 0.0f;
+    // The steps of the stage in work: rows', and with BVEC columns' (16 of
+    // each 32-column tile); prev_a: the last tile's of the stage before.
+    // With BVEC the last tile is summed in its own stage: carrying its
+    // columns' steps over would cost 16 registers that there are not.
+    float sa[FM], prev_a = 0.0f;
+    v4f sb[BVEC ? FN : 1][4];
+    typedef const __attribute__((address_space(3))) float lds_f32;
+    typedef const __attribute__((address_space(3))) v4f lds_v4f;
+    auto read_steps = [&](int s) __attribute__((always_inline)) {
+        uint8_t* at = steps + 4 * s * BT::kSteps;
+        if constexpr (BVEC) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sb[j][q] = *reinterpret_cast<lds_v4f*>(
+                        (lds_void*)(at + 4 * (BM + wn * TN + 32 * j + 8 * q + 4 * (lane >> 5))));
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            sa[i] = *reinterpret_cast<lds_f32*>(
+                (lds_void*)(at + 4 * (wm * TM + 32 * i + (lane & 31))));
+        if constexpr (!BVEC) {
+            const float b = *reinterpret_cast<lds_f32*>(
+                (lds_void*)(at + 4 * (BM + wn * TN / kGroup)));
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] *= b;
+        }
+    };
+    auto fold = [&](v16f& a, const v16f& pt, float fa, const v4f* fb)
+                    __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            if constexpr (BVEC) a[e] = fmaf(pt[e] * fa, fb[e / 4][e % 4], a[e]);
+            else a[e] = fmaf(pt[e], fa, a[e]);
+        }
+    };
+
+    // Substep H of the stage in slot s: its matrix instructions; between
+    // them the reads of the next substep's fragments (slot ns) and loads
+    // [X0, X1) of the refill of slot rs with group rk.
+    constexpr int kFR = FM + FN, kFRPer = (kFR + kMF - 1) / kMF;
+    auto substep = [&](auto hc, int ns, auto x0c, auto x1c, int rs, int rk)
+                       __attribute__((always_inline)) {
+        constexpr int H = decltype(hc)::value;
+        constexpr int X0 = decltype(x0c)::value, X1 = decltype(x1c)::value;
+        constexpr int kDPer = (X1 - X0 + kMF - 1) / kMF;
+        const uint8_t* la = smem + ns * kStage + arow;
+        const uint8_t* lb = smem + ns * kStage + kStageA + brow;
+#pragma unroll
+        for (int t = 0; t < kMF; ++t) {
+            const int i = t % FM, j = t / FM;
+            if constexpr (H == 0) {
+                const v16f zero = {0};
+                static_assert(kMF > 1, "the last tile's registers outlive the first's start");
+                part[t] = mfma_ba<FA, FB>(bf[0][j], af[0][i], zero);
+                if (!BVEC && t == 0)
+                    fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
+            } else {
+                part[t] = mfma_ba<FA, FB>(bf[1][j], af[1][i], part[t]);
+                if (t > 0) {
+                    const int u = t - 1;
+                    fold(acc[u % FM][u / FM], part[u], sa[u % FM], sb[BVEC ? u / FM : 0]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kFRPer; ++q) {
+                const int x = t * kFRPer + q;
+                if (x < FM) af[1 - H][x] = OA::template frag<1 - H>(la + 32 * x * kRowA, aoff[x]);
+                else if (x < kFR)
+                    bf[1 - H][x - FM] =
+                        OB::template frag<1 - H>(lb + 32 * (x - FM) * kRowB, boff[x - FM]);
+            }
+#pragma unroll
+            for (int q = 0; q < kDPer; ++q) {
+                const int x = X0 + t * kDPer + q;
+                if (x < X1) load(x, rs, rk);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (H == 1) {
+            if constexpr (BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], sa[FM - 1], sb[FN - 1]);
+            else prev_a = sa[FM - 1];
+        }
+    };
+    // A refill's loads go out over two substeps when the ring has the slack
+    // (three stages or more): the first kH after the barrier that frees the
+    // slot, the rest in the next stage's first substep.
+    constexpr bool kSplit = ST >= 3;
+    constexpr int kH = kSplit ? (kLoads + 1) / 2 : kLoads;
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using IH = std::integral_constant<int, kH>;
+    using IL = std::integral_constant<int, kLoads>;
+
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s)
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) load(x, s, s);
+#pragma unroll
+    for (int x = 0; x < kH; ++x) load(x, ST - 1, ST - 1);
+    wait_vmcnt<kLoads * (ST - 2) + kH>();
+    barrier();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) af[0][i] = OA::template frag<0>(smem + arow + 32 * i * kRowA, aoff[i]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        bf[0][j] = OB::template frag<0>(smem + kStageA + brow + 32 * j * kRowB, boff[j]);
+
+    for (int t0 = 0; t0 < nk; t0 += ST) {
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+            const int st = t0 + s;
+            if (st >= nk) break;
+            read_steps(s);
+            // the rest of the refill that stage st - 1 began
+            constexpr int kPrevSlot = ST - 1;
+            substep(I0{}, s, IH{}, IL{}, (s + kPrevSlot) % ST, st + ST - 1);
+            wait_vmcnt<kLoads * (ST - 2)>();  // this wave's loads of stage st + 1
+            wait_lgkmcnt0();                  // and its reads of this stage
+            barrier();
+            substep(I1{}, (s + 1) % ST, I0{}, IH{}, s, st + ST);
+        }
+    }
+    if constexpr (!BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
+    wait_vmcnt<0>();  // the prefetches past the end
+
+    // acc[i][j][e] is row m0 + wm*TM + 32i + lane%32, column
+    // n0 + wn*TN + 32j + 8*(e/4) + 4*(lane/32) + e%4.
+    if (p.vec_out16) {
+        // through LDS, as the per-tensor kernel: whole 16-byte chunks per row
+        constexpr int kRowBytes = TN * 2, kChunks = kRowBytes / 16;
+        constexpr int kRowsPerPass = 64 / kChunks, kRegion = TM * kRowBytes;
+        static_assert(NW * kRegion <= ST * kStage, "epilogue staging fits the ring");
+        barrier();
+        uint8_t* wl = smem + wave * kRegion;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int cl = 32 * j + 8 * q + 4 * (lane >> 5);
+                const int64_t gn = n0 + wn * TN + cl;
+                float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (p.bias && gn < p.n) {
+                    const uint2 bb = *reinterpret_cast<const uint2*>(p.bias + gn);
+                    bias[0] = bf16_lo(bb.x); bias[1] = bf16_hi(bb.x);
+                    bias[2] = bf16_lo(bb.y); bias[3] = bf16_hi(bb.y);
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const int row = 32 * i + (lane & 31);
+                    const int chunk = (cl >> 3) ^ (row % kChunks);
+                    v2i pk;
+                    pk[0] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 0] + bias[0],
+                                                 acc[i][j][4 * q + 1] + bias[1]);
+                    pk[1] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 2] + bias[2],
+                                                 acc[i][j][4 * q + 3] + bias[3]);
+                    *reinterpret_cast<__attribute__((address_space(3))) v2i*>(
+                        (lds_void*)(wl + row * kRowBytes + chunk * 16 + 8 * (lane >> 5))) = pk;
+                }
+            }
+        }
+        const int cc = lane % kChunks;
+        const int64_t gn = n0 + wn * TN + 8 * cc;
+#pragma unroll
+        for (int ps = 0; ps < TM / kRowsPerPass; ++ps) {
+            const int row = ps * kRowsPerPass + lane / kChunks;
+            const v4i v = *reinterpret_cast<const __attribute__((address_space(3))) v4i*>(
+                (lds_void*)(wl + row * kRowBytes + ((cc ^ (row % kChunks)) << 4)));
+            const int64_t gm = m0 + wm * TM + row;
+            if (gm < p.m && gn < p.n) *reinterpret_cast<v4i*>(p.out + gm * p.n + gn) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int64_t gn = n0 + wn * TN + 32 * j + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+            if (gn >= p.n) continue;
+            const float bias = p.bias ? bf16_to_f32(p.bias[gn]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int64_t gm = m0 + wm * TM + 32 * i + (lane & 31);
+                if (gm < p.m) p.out[gm * p.n + gn] = f32_to_bf16(acc[i][j][e] + bias);
+            }
+        }
+    }
+}
+
+enum class BlockCfg { kWide, kTall, kMid };
+hipError_t launch_block_nt(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
+hipError_t launch_block_nn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
+hipError_t launch_block_tn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
+
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+hipError_t launch_block_tile(const BlockGemmLaunch& g, hipStream_t stream) {
+    BlockTileParams p{};
+    p.a = g.a;
+    p.b = g.b;
+    p.sa = g.sa;
+    p.sb = g.sb;
+    p.bias = g.bias;
+    p.out = g.out;
+    p.m = g.m;
+    p.n = g.n;
+    p.k = g.k;
+    p.lda = g.lda;
+    p.ldb = g.ldb;
+    p.tiles_m = (int)((g.m + BM - 1) / BM);
+    p.tiles_n = (int)((g.n + BN - 1) / BN);
+    p.group_m = 4;
+    const uintptr_t ob = reinterpret_cast<uintptr_t>(g.out);
+    const uintptr_t bb = reinterpret_cast<uintptr_t>(g.bias);
+    p.vec_out16 = (ob & 15) == 0 && g.n % 8 == 0 && (bb & 7) == 0;
+    const int total = p.tiles_m * p.tiles_n;
+    p.xcd_remap = total % 8 == 0;
+    hipLaunchKernelGGL((block_gemm_kernel<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST>),
+                       dim3((unsigned)total), dim3(WM * WN * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC>
+hipError_t launch_block_cfg(const BlockGemmLaunch& g, BlockCfg c, hipStream_t stream) {
+    switch (c) {
+        case BlockCfg::kWide:
+            return launch_block_tile<FA, FB, AMN, BMN, BVEC, 128, 256, 2, 4, 3>(g, stream);
+        case BlockCfg::kTall:
+            return launch_block_tile<FA, FB, AMN, BMN, BVEC, 256, 128, 4, 2, 3>(g, stream);
+        default: break;
+    }
+    return launch_block_tile<FA, FB, AMN, BMN, BVEC, 128, 128, 4, 2, 4>(g, stream);
+}
+
+// Formats of one layout's instances: equal ones, and an E5M2 first operand
+// with an E4M3 second (a gradient times what the forward quantized).
+template <bool AMN, bool BMN>
+hipError_t launch_block_layout(const BlockGemmLaunch& g, bool bvec, BlockCfg c,
+                               hipStream_t stream) {
+    auto pick = [&](auto bv) {
+        constexpr bool V = decltype(bv)::value;
+        if (g.fmt_a == 0) return launch_block_cfg<0, 0, AMN, BMN, V>(g, c, stream);
+        return g.fmt_b == 0 ? launch_block_cfg<1, 0, AMN, BMN, V>(g, c, stream)
+                            : launch_block_cfg<1, 1, AMN, BMN, V>(g, c, stream);
+    };
+    return bvec ? pick(std::true_type{}) : pick(std::false_type{});
+}
+
+}  // namespace fp8lin
