@@ -7,8 +7,11 @@
 // experts' weights once (3 dim hidden bytes each), so both products are
 // shaped for that:
 //
-//  * A workgroup takes 16 hidden units of one expert (16 rows of G and of U)
-//    or 32 rows of W2, for all of the expert's tokens; its 4 waves take the
+//  * The routing launch leaves a list of the experts that were reached and
+//    of each one's tokens, so that a workgroup of the products knows its work
+//    from one short read.
+//  * A workgroup takes 32 hidden units of one expert (32 rows of G and of U)
+//    or 64 rows of W2, for all of the expert's tokens; its 4 waves take the
 //    128-k blocks in turn, so every byte of x and of the weights is loaded by
 //    one wave of it, and the four partial sums meet in LDS in a fixed order.
 //  * Weights go straight into registers in the matrix instruction's layout
@@ -21,6 +24,8 @@
 //    each (the value rounded, and the rest rounded): 16 bits of precision
 //    for one more matrix instruction, which the loads hide.
 
+#include <type_traits>
+
 #include "block.hpp"
 #include "common.hpp"
 
@@ -31,17 +36,29 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxExperts = 512, kMaxTokens = 1024;
-constexpr int kRouteTokens = 8;   // tokens of a routing workgroup
-constexpr int kUnits = 16;        // hidden units of a gate / up workgroup
-constexpr int kRows = 32;         // rows of W2 of a down workgroup
+constexpr int kRouteTokens = 4;   // tokens of a routing workgroup
+constexpr int kTiles = 4;         // 16-row tiles of weights per wave
+constexpr int kUnits = 32;        // hidden units of a gate / up workgroup
+constexpr int kRows = 64;         // rows of W2 of a down workgroup
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// An expert that some token chose: its slots (token * top_k + rank) are
+// slots[first .. first + count), in no particular order (each is a column of
+// its own in the products).
+struct Reached {
+    int expert, first, count, pad;
+};
 
 // Workspace: counters first (zero between calls), then what one kernel
 // leaves for the next.
 struct MoeWs {
     uint32_t* route_count;  // per token group: routing workgroups done
-    uint32_t* down_count;   // per 32 rows of the output: experts done
+    uint32_t* group_count;  // token groups done
+    uint32_t* down_count;   // per kRows of the output: experts done
+    int32_t* reached_n;     // experts reached
+    Reached* reached;       // [min(experts, tokens * top_k)]
+    int32_t* slots;         // [tokens * top_k]
     float* logits;          // [tokens][experts]
     int32_t* ids;           // [tokens][top_k]
     float* weights;         // [tokens][top_k]
@@ -53,7 +70,7 @@ struct MoeWs {
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Counters have a fixed place, so that calls of different shapes can share a
-// workspace: kMaxTokens / kRouteTokens and 65536 / kRows words.
+// workspace.
 MoeWs layout(void* ws, int64_t t, int64_t e, int64_t k, int64_t d, int64_t h, size_t* total) {
     uint8_t* p = static_cast<uint8_t*>(ws);
     size_t at = 0;
@@ -64,7 +81,11 @@ MoeWs layout(void* ws, int64_t t, int64_t e, int64_t k, int64_t d, int64_t h, si
     };
     MoeWs w;
     w.route_count = reinterpret_cast<uint32_t*>(take(4 * (kMaxTokens / kRouteTokens)));
+    w.group_count = reinterpret_cast<uint32_t*>(take(4));
     w.down_count = reinterpret_cast<uint32_t*>(take(4 * (65536 / kRows)));
+    w.reached_n = reinterpret_cast<int32_t*>(take(4));
+    w.reached = reinterpret_cast<Reached*>(take(sizeof(Reached) * e));
+    w.slots = reinterpret_cast<int32_t*>(take(4 * t * k));
     w.logits = reinterpret_cast<float*>(take(4 * t * e));
     w.ids = reinterpret_cast<int32_t*>(take(4 * t * k));
     w.weights = reinterpret_cast<float*>(take(4 * t * k));
@@ -78,10 +99,12 @@ MoeWs layout(void* ws, int64_t t, int64_t e, int64_t k, int64_t d, int64_t h, si
 // Values that workgroups of one launch hand to each other go through memory
 // at device scope: stored and loaded there, and a store has reached it when
 // the wave's count of outstanding stores is zero.
-__device__ __forceinline__ void store_dev(float* p, float v) {
+template <class T>
+__device__ __forceinline__ void store_dev(T* p, T v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ float load_dev(const float* p) {
+template <class T>
+__device__ __forceinline__ T load_dev(const T* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void stores_done() {
@@ -104,69 +127,172 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t of, uint32_t
     return *flag != 0;
 }
 
-// Top-k of one token by one wave: logits in LDS.
+// Reductions over a wave by lane permutes inside the vector unit (shifts by
+// 1, 2, 4, 8 in rows of 16 lanes, then the rows' last lanes to the next
+// rows): the full result is lane 63's.  `id` leaves the other operand as it
+// is.
+template <class Op>
+__device__ __forceinline__ float wave_reduce(float v, float id, Op op) {
+    auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+        const int o = __builtin_amdgcn_update_dpp(__float_as_int(id), __float_as_int(v),
+                                                  decltype(ctrl)::value, decltype(rows)::value,
+                                                  0xf, false);
+        v = op(v, __int_as_float(o));
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float reduce_max(float v) {
+    return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float reduce_sum(float v) {
+    return wave_reduce(v, 0.0f, [](float a, float b) { return a + b; });
+}
+
+// Top-k of one token by one wave.  Lane l has the logits of experts
+// l * PER .. l * PER + PER - 1 (v[], -inf past the last), so the lowest lane
+// that holds the maximum, at its first place, is the lowest index.
+template <int PER>
 __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& ws, int64_t t,
-                                               const float* logit, int lane) {
+                                               float (&v)[PER], int lane) {
     float mx = -INFINITY, sum = 0.0f;
-    for (int e = lane; e < p.experts; e += kWave) mx = fmaxf(mx, logit[e]);
-    mx = wave_max(mx);
-    for (int e = lane; e < p.experts; e += kWave) sum += expf(logit[e] - mx);
-    sum = wave_sum(sum);
-    uint32_t taken = 0;  // bit i: this lane's expert lane + 64 i is taken
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mx = fmaxf(mx, v[i]);
+    mx = reduce_max(mx);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (lane * PER + i < p.experts) sum += expf(v[i] - mx);
+    sum = reduce_sum(sum);
+    // A NaN logit ranks with -inf, below every number; what is taken, and
+    // what is no expert, ranks below that.
+    const float taken = -INFINITY;
+    uint32_t left = 0;  // bit i: expert i of this lane can still be taken
+    bool nan[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        nan[i] = v[i] != v[i];
+        if (nan[i]) v[i] = taken;
+        if (lane * PER + i < p.experts) left |= 1u << i;
+    }
     float chosen = 0.0f, total = 0.0f;
     int chosen_id = 0;
     for (int j = 0; j < p.top_k; ++j) {
         float best = -INFINITY;
-        int at = kMaxExperts;  // NaN and -inf logits lose to any other, lowest index first
-        for (int e = lane, i = 0; e < p.experts; e += kWave, ++i) {
-            if (taken >> i & 1) continue;
-            const float v = logit[e] == logit[e] ? logit[e] : -INFINITY;
-            if (at == kMaxExperts || v > best) best = v, at = e;
-        }
+        int at = -1;
 #pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const float ov = __shfl_xor(best, off, kWave);
-            const int oa = __shfl_xor(at, off, kWave);
-            if (oa < kMaxExperts && (at == kMaxExperts || ov > best || (ov == best && oa < at)))
-                best = ov, at = oa;
-        }
-        if (at % kWave == lane) taken |= 1u << (at / kWave);
-        const float w = expf(logit[at] - mx) / sum;
+        for (int i = PER - 1; i >= 0; --i)
+            if ((left >> i & 1) && (at < 0 || v[i] >= best)) best = v[i], at = i;
+        const float top = reduce_max(best);
+        const uint64_t who = __ballot(at >= 0 && best == top);
+        const int winner = __ffsll((unsigned long long)who) - 1;
+        const bool mine = lane == winner;
+        float value = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i == at) value = nan[i] ? NAN : v[i];
+        const int id = __builtin_amdgcn_readlane(lane * PER + at, winner);
+        value = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), winner));
+        if (mine) left &= ~(1u << at);
+        const float w = expf(value - mx) / sum;
         total += w;
-        if (lane == j) chosen = w, chosen_id = at;
+        if (lane == j) chosen = w, chosen_id = id;
     }
     if (lane < p.top_k) {
         const float w = p.renorm ? chosen / total : chosen;
         const int64_t o = t * p.top_k + lane;
-        ws.ids[o] = chosen_id;
+        store_dev(ws.ids + o, chosen_id);
         ws.weights[o] = w;
         if (p.ids) p.ids[o] = chosen_id;
         if (p.weights) p.weights[o] = w;
     }
 }
 
-// A workgroup computes the logits of 4 experts (one a wave) for 8 tokens;
-// the last of a token group's workgroups selects its experts.
+template <int PER>
+__device__ __forceinline__ void load_and_select(const MoeLaunch& p, const MoeWs& ws, int64_t t,
+                                                int lane) {
+    float v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane * PER + i;
+        v[i] = e < p.experts ? load_dev(ws.logits + t * p.experts + e) : -INFINITY;
+    }
+    select_experts<PER>(p, ws, t, v, lane);
+}
+
+// The list of reached experts and their slots, by one workgroup.
+struct Lists {
+    int count[kMaxExperts], first[kMaxExperts];
+    int sums[2][kWaves];
+};
+__device__ __forceinline__ void build_lists(const MoeLaunch& p, const MoeWs& ws, Lists& s) {
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int n = p.tokens * p.top_k;
+    for (int e = tid; e < kMaxExperts; e += kThreads) s.count[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) atomicAdd(&s.count[load_dev(ws.ids + i)], 1);
+    __syncthreads();
+    // each thread takes two neighbouring experts: slots and reached ones before them
+    static_assert(kMaxExperts == 2 * kThreads, "two experts per thread");
+    const int c0 = s.count[2 * tid], c1 = s.count[2 * tid + 1];
+    int slots = c0 + c1, used = (c0 > 0) + (c1 > 0);
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int a = __shfl_up(slots, off, kWave), b = __shfl_up(used, off, kWave);
+        if (lane >= off) slots += a, used += b;
+    }
+    if (lane == kWave - 1) s.sums[0][wave] = slots, s.sums[1][wave] = used;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) slots += s.sums[0][w], used += s.sums[1][w];
+        all += s.sums[1][w];
+    }
+    const int f0 = slots - c0 - c1, f1 = slots - c1;
+    int u = used - (c0 > 0) - (c1 > 0);
+    if (c0 > 0) ws.reached[u++] = Reached{2 * tid, f0, c0, 0};
+    if (c1 > 0) ws.reached[u] = Reached{2 * tid + 1, f1, c1, 0};
+    s.first[2 * tid] = f0;
+    s.first[2 * tid + 1] = f1;
+    if (tid == 0) *ws.reached_n = all;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads)
+        ws.slots[atomicAdd(&s.first[load_dev(ws.ids + i)], 1)] = i;
+}
+
+// A workgroup computes the logits of 4 experts (one a wave) for 4 tokens;
+// the last of a token group's workgroups selects its experts (a token a
+// wave), and the last of those writes the lists.
 __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs ws) {
-    __shared__ float logit[kWaves][kMaxExperts];
+    static_assert(kRouteTokens == kWaves, "a token per wave");
+    __shared__ Lists lists;
     __shared__ uint32_t flag;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int t0 = blockIdx.y * kRouteTokens;
-    const int nt = p.tokens - t0 < kRouteTokens ? p.tokens - t0 : kRouteTokens;
     const int e = blockIdx.x * kWaves + wave;
     if (e < p.experts) {
+        const uint16_t* r = p.router + (int64_t)e * p.dim;
+        const uint16_t* x[kRouteTokens];
         float acc[kRouteTokens];
 #pragma unroll
-        for (int i = 0; i < kRouteTokens; ++i) acc[i] = 0.0f;
-        const uint16_t* r = p.router + (int64_t)e * p.dim;
-        const uint16_t* x = p.x + (int64_t)t0 * p.dim;
+        for (int i = 0; i < kRouteTokens; ++i) {
+            // (past the last token: the last again, not stored)
+            const int t = t0 + i < p.tokens ? t0 + i : p.tokens - 1;
+            x[i] = p.x + (int64_t)t * p.dim;
+            acc[i] = 0.0f;
+        }
+#pragma unroll 4
         for (int d = 8 * lane; d < p.dim; d += 8 * kWave) {  // dim is a multiple of 16
             const uint4 rv = *reinterpret_cast<const uint4*>(r + d);
             const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
             for (int i = 0; i < kRouteTokens; ++i) {
-                if (i >= nt) break;
-                const uint4 xv = *reinterpret_cast<const uint4*>(x + (int64_t)i * p.dim + d);
+                const uint4 xv = *reinterpret_cast<const uint4*>(x[i] + d);
                 const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -177,71 +303,20 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs 
         }
 #pragma unroll
         for (int i = 0; i < kRouteTokens; ++i) {
-            if (i >= nt) break;
-            const float s = wave_sum(acc[i]);
-            if (lane == 0) store_dev(ws.logits + (int64_t)(t0 + i) * p.experts + e, s);
+            const float s = reduce_sum(acc[i]);
+            if (lane == 0 && t0 + i < p.tokens)
+                store_dev(ws.logits + (int64_t)(t0 + i) * p.experts + e, s);
         }
     }
     if (!last_of(ws.route_count + blockIdx.y, gridDim.x, &flag)) return;
-    for (int i = wave; i < nt; i += kWaves) {
-        for (int j = lane; j < p.experts; j += kWave)
-            logit[wave][j] = load_dev(ws.logits + (int64_t)(t0 + i) * p.experts + j);
-        // one wave writes and reads these: its LDS accesses are in order
-        select_experts(p, ws, t0 + i, logit[wave], lane);
+    const int t = t0 + wave;
+    if (t < p.tokens) {
+        if (p.experts <= kWave) load_and_select<1>(p, ws, t, lane);
+        else if (p.experts <= 2 * kWave) load_and_select<2>(p, ws, t, lane);
+        else load_and_select<8>(p, ws, t, lane);
     }
-}
-
-// The u-th expert (by index) that any token chose, and its slots (token *
-// top_k + rank) in order.  Every lane calls it; -1: there are fewer.
-struct Picked {
-    uint32_t mask[kMaxExperts / 32];
-    uint32_t wave_count[kWaves];
-    uint16_t slot[kMaxTokens];
-};
-__device__ __forceinline__ int pick_expert(const int32_t* ids, int n, int u, Picked& s,
-                                           int& count, int& reached) {
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    if (tid < kMaxExperts / 32) s.mask[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-        const int e = ids[i];
-        atomicOr(&s.mask[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    int expert = -1, before = 0;
-    for (int w = 0; w < kMaxExperts / 32; ++w) {
-        uint32_t m = s.mask[w];
-        const int c = __popc(m);
-        if (u >= before && u < before + c) {
-            for (int skip = u - before; skip > 0; --skip) m &= m - 1;
-            expert = 32 * w + __ffs(m) - 1;
-        }
-        before += c;
-    }
-    reached = before;
-    if (expert < 0) return -1;
-    // each wave takes a quarter of the slots, in order
-    const int per = (n + kThreads - 1) / kThreads * kWave;
-    const int b = wave * per, e = b + per < n ? b + per : n;
-    int c = 0;
-    for (int i = b; i < e; i += kWave)
-        c += __popcll(__ballot(i + lane < e && ids[i + lane] == expert));
-    if (lane == 0) s.wave_count[wave] = c;
-    __syncthreads();
-    int at = 0;
-    count = 0;
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) at += s.wave_count[w];
-        count += s.wave_count[w];
-    }
-    for (int i = b; i < e; i += kWave) {
-        const bool hit = i + lane < e && ids[i + lane] == expert;
-        const uint64_t m = __ballot(hit);
-        if (hit) s.slot[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
-        at += __popcll(m);
-    }
-    __syncthreads();
-    return expert;
+    if (!last_of(ws.group_count, gridDim.y, &flag)) return;
+    build_lists(p, ws, lists);
 }
 
 // Eight fp8 codes -> bf16 (exact).
@@ -274,22 +349,22 @@ __device__ __forceinline__ bf16x8 as_bf16(const uint4& v) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// Two 16-row tiles of weights times the activations of 16 tokens over the
+// kTiles 16-row tiles of weights times the activations of 16 tokens over the
 // 128-k blocks wave, wave + 4, ... of `kdim`: acc[tile] += step * sum.
 // Lane l holds rows l % 16 and k = 64 i + 16 (l / 16) .. + 15 of a block (i =
 // 0, 1) on both sides, which is a reordering of k that the sum does not see.
 //   w[tile]: this lane's row at its first k;  s[tile]: the tile's steps.
 //   act[ACT]: the token's activations (added: the lane's rest, if any).
 template <int FMT, int ACT>
-__device__ __forceinline__ void tile_products(const uint8_t* const (&w)[2],
-                                              const float* const (&s)[2],
+__device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
+                                              const float* const (&s)[kTiles],
                                               const uint16_t* const (&act)[ACT], int kdim,
-                                              int wave, int lane, v4f (&acc)[2]) {
+                                              int wave, int lane, v4f (&acc)[kTiles]) {
     const int kq = 16 * (lane / 16);
     struct Block {
-        uint4 w[2][2];
+        uint4 w[kTiles][2];
         uint4 x[ACT][2][2];
-        float s[2];
+        float s[kTiles];
     };
     auto load = [&](int b, Block& k) __attribute__((always_inline)) {
         const bool whole = kGroup * (b + 1) <= kdim;  // uniform
@@ -300,7 +375,7 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[2],
             const bool in = whole || k0 + kq < kdim;
             const int at = in ? k0 : -kq;  // (one that exists instead)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) k.w[t][i] = *reinterpret_cast<const uint4*>(w[t] + at);
+            for (int t = 0; t < kTiles; ++t) k.w[t][i] = *reinterpret_cast<const uint4*>(w[t] + at);
 #pragma unroll
             for (int a = 0; a < ACT; ++a) {
                 k.x[a][i][0] = *reinterpret_cast<const uint4*>(act[a] + at);
@@ -314,17 +389,17 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[2],
                     v.w = in ? v.w : 0u;
                 };
 #pragma unroll
-                for (int t = 0; t < 2; ++t) keep(k.w[t][i]);
+                for (int t = 0; t < kTiles; ++t) keep(k.w[t][i]);
 #pragma unroll
                 for (int a = 0; a < ACT; ++a) keep(k.x[a][i][0]), keep(k.x[a][i][1]);
             }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) k.s[t] = s[t][b];
+        for (int t = 0; t < kTiles; ++t) k.s[t] = s[t][b];
     };
     auto multiply = [&](const Block& k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kTiles; ++t) {
             v4f part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -352,19 +427,20 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[2],
     }
 }
 
-// The waves' sums of a 2 x 16 x 16 result, added in wave order: thread
-// (token = tid / 16, row = tid % 16) gets both tiles' values.  acc[t][i] is
+// The waves' sums of a kTiles x 16 x 16 result, added in wave order: thread
+// (token = tid / 16, row = tid % 16) gets every tile's value.  acc[t][i] is
 // row 4 (lane / 16) + i, token lane % 16.
-typedef float Partial[kWaves][2][16][17];
-__device__ __forceinline__ void join_waves(const v4f (&acc)[2], Partial& red, float (&out)[2]) {
+typedef float Partial[kWaves][kTiles][16][17];
+__device__ __forceinline__ void join_waves(const v4f (&acc)[kTiles], Partial& red,
+                                           float (&out)[kTiles]) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[wave][t][lane % 16][4 * (lane / 16) + i] = acc[t][i];
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
         float v = red[0][t][tid / 16][tid % 16];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) v += red[w][t][tid / 16][tid % 16];
@@ -375,91 +451,111 @@ __device__ __forceinline__ void join_waves(const v4f (&acc)[2], Partial& red, fl
 
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeWs ws) {
-    __shared__ Picked picked;
     __shared__ Partial red;
-    int count = 0, reached;
-    const int64_t e = __builtin_amdgcn_readfirstlane(
-        pick_expert(ws.ids, p.tokens * p.top_k, blockIdx.y, picked, count, reached));
-    if (e < 0) return;
+    if ((int)blockIdx.y >= *ws.reached_n) return;
+    const Reached work = ws.reached[blockIdx.y];
+    const int64_t e = work.expert;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int f0 = blockIdx.x * kUnits;
     const int kg = (p.dim + kGroup - 1) / kGroup, rg = (2 * p.hidden + kGroup - 1) / kGroup;
-    const uint8_t* w[2];
-    const float* s[2];
+    const uint8_t* w[kTiles];  // gate, gate, up, up
+    const float* s[kTiles];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {  // 16 rows share a tile of steps: hidden is a multiple of 16
-        const int row = f0 + t * p.hidden;
+    for (int t = 0; t < kTiles; ++t) {
+        // 16 rows share a tile of steps (hidden is a multiple of 16); a second
+        // 16 units past the last repeat the first
+        const int f = f0 + 16 * (t % 2) < p.hidden ? f0 + 16 * (t % 2) : f0;
+        const int row = f + t / 2 * p.hidden;
         w[t] = p.w13 + (e * 2 * p.hidden + row + lane % 16) * p.dim + 16 * (lane / 16);
         s[t] = p.s13 + (e * rg + row / kGroup) * kg;
     }
-    for (int c0 = 0; c0 < count; c0 += 16) {
+    for (int c0 = 0; c0 < work.count; c0 += 16) {
         // lanes past the list repeat its last token; their results are dropped
-        const int c = c0 + lane % 16 < count ? c0 + lane % 16 : count - 1;
-        const uint16_t* const x[1] = {p.x + (int64_t)(picked.slot[c] / p.top_k) * p.dim +
+        const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
+        const int slot = ws.slots[work.first + c];
+        const uint16_t* const x[1] = {p.x + (int64_t)(slot / p.top_k) * p.dim +
                                       16 * (lane / 16)};
-        v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        v4f acc[kTiles] = {};
         tile_products<FMT, 1>(w, s, x, p.dim, wave, lane, acc);
-        float v[2];
+        float v[kTiles];
         join_waves(acc, red, v);
-        if (c0 + tid / 16 < count) {
-            const float h = v[0] / (1.0f + expf(-v[0])) * v[1];
-            const int64_t o = (int64_t)picked.slot[c0 + tid / 16] * p.hidden + f0 + tid % 16;
-            const uint16_t hi = f32_to_bf16(h);
-            ws.h_hi[o] = hi;
-            ws.h_lo[o] = f32_to_bf16(h - bf16_to_f32(hi));
+        if (c0 + tid / 16 < work.count) {
+            const int64_t o = (int64_t)ws.slots[work.first + c0 + tid / 16] * p.hidden + f0 +
+                              tid % 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float h = v[i] / (1.0f + expf(-v[i])) * v[2 + i];
+                const uint16_t hi = f32_to_bf16(h);
+                if (f0 + 16 * i < p.hidden) {
+                    ws.h_hi[o + 16 * i] = hi;
+                    ws.h_lo[o + 16 * i] = f32_to_bf16(h - bf16_to_f32(hi));
+                }
+            }
         }
     }
 }
 
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs ws) {
-    __shared__ Picked picked;
     __shared__ Partial red;
     __shared__ uint32_t flag;
-    int count = 0, reached;
-    const int64_t e = __builtin_amdgcn_readfirstlane(
-        pick_expert(ws.ids, p.tokens * p.top_k, blockIdx.y, picked, count, reached));
-    if (e < 0) return;
+    const int reached = *ws.reached_n;
+    if ((int)blockIdx.y >= reached) return;
+    const Reached work = ws.reached[blockIdx.y];
+    const int64_t e = work.expert;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int d0 = blockIdx.x * kRows;
     const int kg = (p.hidden + kGroup - 1) / kGroup, rg = (p.dim + kGroup - 1) / kGroup;
-    const uint8_t* w[2];
-    const float* s[2];
+    const uint8_t* w[kTiles];
+    const float* s[kTiles];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        // dim is a multiple of 16: a second tile past it repeats the first
+    for (int t = 0; t < kTiles; ++t) {
+        // dim is a multiple of 16: a tile past it repeats the first
         const int row = d0 + 16 * t < p.dim ? d0 + 16 * t : d0;
         w[t] = p.w2 + (e * p.dim + row + lane % 16) * p.hidden + 16 * (lane / 16);
         s[t] = p.s2 + (e * rg + row / kGroup) * kg;
     }
-    for (int c0 = 0; c0 < count; c0 += 16) {
-        const int c = c0 + lane % 16 < count ? c0 + lane % 16 : count - 1;
-        const int64_t at = (int64_t)picked.slot[c] * p.hidden + 16 * (lane / 16);
+    for (int c0 = 0; c0 < work.count; c0 += 16) {
+        const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
+        const int64_t at = (int64_t)ws.slots[work.first + c] * p.hidden + 16 * (lane / 16);
         const uint16_t* const h[2] = {ws.h_hi + at, ws.h_lo + at};
-        v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        v4f acc[kTiles] = {};
         tile_products<FMT, 2>(w, s, h, p.hidden, wave, lane, acc);
-        float v[2];
+        float v[kTiles];
         join_waves(acc, red, v);
-        if (c0 + tid / 16 < count) {
-            float* o = ws.part + (int64_t)picked.slot[c0 + tid / 16] * p.dim + d0 + tid % 16;
-            store_dev(o, v[0]);
-            if (d0 + 16 < p.dim) store_dev(o + 16, v[1]);
+        if (c0 + tid / 16 < work.count) {
+            float* o = ws.part + (int64_t)ws.slots[work.first + c0 + tid / 16] * p.dim + d0 +
+                       tid % 16;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                if (d0 + 16 * t < p.dim) store_dev(o + 16 * t, v[t]);
         }
     }
-    // The last of the reached experts at these rows adds up every token's.
+    // The last of the reached experts at these rows adds up every token's, in
+    // the order of its choices: two outputs a thread, eight loads in flight.
     if (!last_of(ws.down_count + blockIdx.x, reached, &flag)) return;
-    const int cols = p.dim - d0 < kRows ? p.dim - d0 : kRows;
-    for (int i = tid; i < p.tokens * kRows; i += kThreads) {
-        const int t = i / kRows, d = i % kRows;
-        if (d >= cols) continue;
-        float y = 0.0f;
-        for (int j = 0; j < p.top_k; ++j) {
-            const int64_t slot = (int64_t)t * p.top_k + j;
-            y = fmaf(ws.weights[slot], load_dev(ws.part + slot * p.dim + d0 + d), y);
+    const int d = d0 + 2 * (tid % (kRows / 2));
+    if (d >= p.dim) return;
+    for (int t = tid / (kRows / 2); t < p.tokens; t += kThreads / (kRows / 2)) {
+        float y0 = 0.0f, y1 = 0.0f;
+        for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+            uint64_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t slot = (int64_t)t * p.top_k + (j0 + j < p.top_k ? j0 + j : j0);
+                v[j] = load_dev(reinterpret_cast<const uint64_t*>(ws.part + slot * p.dim + d));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j0 + j >= p.top_k) break;
+                const float w = ws.weights[(int64_t)t * p.top_k + j0 + j];
+                y0 = fmaf(w, __uint_as_float((uint32_t)v[j]), y0);
+                y1 = fmaf(w, __uint_as_float((uint32_t)(v[j] >> 32)), y1);
+            }
         }
-        p.out[(int64_t)t * p.dim + d0 + d] = f32_to_bf16(y);
+        *reinterpret_cast<uint32_t*>(p.out + (int64_t)t * p.dim + d) = f32x2_to_bf16x2(y0, y1);
     }
 }
 
@@ -482,7 +578,7 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const int slots = p.tokens * p.top_k;
     const int reach = slots < p.experts ? slots : p.experts;  // at most so many experts
-    const dim3 up(p.hidden / kUnits, reach), down((p.dim + kRows - 1) / kRows, reach);
+    const dim3 up((p.hidden + kUnits - 1) / kUnits, reach), down((p.dim + kRows - 1) / kRows, reach);
     if (p.fmt == 0) hipLaunchKernelGGL(moe_gate_up_kernel<0>, up, dim3(kThreads), 0, stream, p, ws);
     else hipLaunchKernelGGL(moe_gate_up_kernel<1>, up, dim3(kThreads), 0, stream, p, ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
