@@ -55,7 +55,7 @@ struct Reached {
 struct MoeWs {
     uint32_t* route_count;  // per token group: routing workgroups done
     uint32_t* group_count;  // token groups done
-    uint32_t* down_count;   // per kRows of the output: experts done
+    uint32_t* down_count;   // per kRows of the output and token: experts done
     int32_t* reached_n;     // experts reached
     Reached* reached;       // [min(experts, tokens * top_k)]
     int32_t* slots;         // [tokens * top_k]
@@ -82,7 +82,7 @@ MoeWs layout(void* ws, int64_t t, int64_t e, int64_t k, int64_t d, int64_t h, si
     MoeWs w;
     w.route_count = reinterpret_cast<uint32_t*>(take(4 * (kMaxTokens / kRouteTokens)));
     w.group_count = reinterpret_cast<uint32_t*>(take(4));
-    w.down_count = reinterpret_cast<uint32_t*>(take(4 * (65536 / kRows)));
+    w.down_count = reinterpret_cast<uint32_t*>(take(4 * kMaxTokens * (65536 / kRows)));
     w.reached_n = reinterpret_cast<int32_t*>(take(4));
     w.reached = reinterpret_cast<Reached*>(take(sizeof(Reached) * e));
     w.slots = reinterpret_cast<int32_t*>(take(4 * t * k));
@@ -286,18 +286,32 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs 
             x[i] = p.x + (int64_t)t * p.dim;
             acc[i] = 0.0f;
         }
-#pragma unroll 4
-        for (int d = 8 * lane; d < p.dim; d += 8 * kWave) {  // dim is a multiple of 16
-            const uint4 rv = *reinterpret_cast<const uint4*>(r + d);
-            const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
+        // 2048 k a round, all their loads ahead of the first product; lanes past
+        // dim (a multiple of 16) read what exists and drop it
+        constexpr int kStep = 8 * kWave, kAhead = 4;
+        for (int d0 = 0; d0 < p.dim; d0 += kAhead * kStep) {
+            uint4 rv[kAhead], xv[kAhead][kRouteTokens];
 #pragma unroll
-            for (int i = 0; i < kRouteTokens; ++i) {
-                const uint4 xv = *reinterpret_cast<const uint4*>(x[i] + d);
-                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int a = 0; a < kAhead; ++a) {
+                const int d = d0 + a * kStep + 8 * lane;
+                const int at = d < p.dim ? d : 0;
+                rv[a] = *reinterpret_cast<const uint4*>(r + at);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[i] = fmaf(bf16_lo(xw[j]), bf16_lo(rw[j]), acc[i]);
-                    acc[i] = fmaf(bf16_hi(xw[j]), bf16_hi(rw[j]), acc[i]);
+                for (int i = 0; i < kRouteTokens; ++i)
+                    xv[a][i] = *reinterpret_cast<const uint4*>(x[i] + at);
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                if (d0 + a * kStep + 8 * lane >= p.dim) continue;
+                const uint32_t rw[4] = {rv[a].x, rv[a].y, rv[a].z, rv[a].w};
+#pragma unroll
+                for (int i = 0; i < kRouteTokens; ++i) {
+                    const uint32_t xw[4] = {xv[a][i].x, xv[a][i].y, xv[a][i].z, xv[a][i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i] = fmaf(bf16_lo(xw[j]), bf16_lo(rw[j]), acc[i]);
+                        acc[i] = fmaf(bf16_hi(xw[j]), bf16_hi(rw[j]), acc[i]);
+                    }
                 }
             }
         }
@@ -315,7 +329,12 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs 
         else if (p.experts <= 2 * kWave) load_and_select<2>(p, ws, t, lane);
         else load_and_select<8>(p, ws, t, lane);
     }
-    if (!last_of(ws.group_count, gridDim.y, &flag)) return;
+    if (gridDim.y == 1) {  // this workgroup chose for every token
+        stores_done();
+        __syncthreads();
+    } else if (!last_of(ws.group_count, gridDim.y, &flag)) {
+        return;
+    }
     build_lists(p, ws, lists);
 }
 
@@ -496,12 +515,15 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
     }
 }
 
+// A workgroup's outputs for a token are one expert's share; the workgroup
+// that brings the last of the token's shares for these rows adds them up, in
+// the order of the token's choices (so the result does not depend on which
+// came last).
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
-    __shared__ uint32_t flag;
-    const int reached = *ws.reached_n;
-    if ((int)blockIdx.y >= reached) return;
+    __shared__ int done[16];  // tokens of this round that are complete, else -1
+    if ((int)blockIdx.y >= *ws.reached_n) return;
     const Reached work = ws.reached[blockIdx.y];
     const int64_t e = work.expert;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -532,30 +554,46 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs w
             for (int t = 0; t < kTiles; ++t)
                 if (d0 + 16 * t < p.dim) store_dev(o + 16 * t, v[t]);
         }
-    }
-    // The last of the reached experts at these rows adds up every token's, in
-    // the order of its choices: two outputs a thread, eight loads in flight.
-    if (!last_of(ws.down_count + blockIdx.x, reached, &flag)) return;
-    const int d = d0 + 2 * (tid % (kRows / 2));
-    if (d >= p.dim) return;
-    for (int t = tid / (kRows / 2); t < p.tokens; t += kThreads / (kRows / 2)) {
-        float y0 = 0.0f, y1 = 0.0f;
-        for (int j0 = 0; j0 < p.top_k; j0 += 8) {
-            uint64_t v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t slot = (int64_t)t * p.top_k + (j0 + j < p.top_k ? j0 + j : j0);
-                v[j] = load_dev(reinterpret_cast<const uint64_t*>(ws.part + slot * p.dim + d));
+        stores_done();
+        __syncthreads();
+        if (tid < 16) {
+            int complete = -1;
+            if (c0 + tid < work.count) {
+                const int t = ws.slots[work.first + c0 + tid] / p.top_k;
+                uint32_t* n = ws.down_count + (int64_t)blockIdx.x * kMaxTokens + t;
+                const uint32_t seen = __hip_atomic_fetch_add(n, 1u, __ATOMIC_RELAXED,
+                                                             __HIP_MEMORY_SCOPE_AGENT);
+                if (seen == (uint32_t)p.top_k - 1) {
+                    complete = t;
+                    store_dev(n, 0u);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j0 + j >= p.top_k) break;
-                const float w = ws.weights[(int64_t)t * p.top_k + j0 + j];
-                y0 = fmaf(w, __uint_as_float((uint32_t)v[j]), y0);
-                y1 = fmaf(w, __uint_as_float((uint32_t)(v[j] >> 32)), y1);
-            }
+            done[tid] = complete;
         }
-        *reinterpret_cast<uint32_t*>(p.out + (int64_t)t * p.dim + d) = f32x2_to_bf16x2(y0, y1);
+        __syncthreads();
+        // two outputs a thread, 8 tokens at a time, eight loads in flight
+        const int d = d0 + 2 * (tid % (kRows / 2));
+        for (int i = tid / (kRows / 2); i < 16; i += kThreads / (kRows / 2)) {
+            const int t = done[i];
+            if (t < 0 || d >= p.dim) continue;
+            float y0 = 0.0f, y1 = 0.0f;
+            for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+                uint64_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int64_t slot = (int64_t)t * p.top_k + (j0 + j < p.top_k ? j0 + j : j0);
+                    u[j] = load_dev(reinterpret_cast<const uint64_t*>(ws.part + slot * p.dim + d));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (j0 + j >= p.top_k) break;
+                    const float g = ws.weights[(int64_t)t * p.top_k + j0 + j];
+                    y0 = fmaf(g, __uint_as_float((uint32_t)u[j]), y0);
+                    y1 = fmaf(g, __uint_as_float((uint32_t)(u[j] >> 32)), y1);
+                }
+            }
+            *reinterpret_cast<uint32_t*>(p.out + (int64_t)t * p.dim + d) = f32x2_to_bf16x2(y0, y1);
+        }
     }
 }
 
