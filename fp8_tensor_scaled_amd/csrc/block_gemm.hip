@@ -5,11 +5,9 @@
 // product of the two steps and added to the running sum (one rounding of
 // the product of the steps, one fused multiply-add per group).
 //
-// This file holds the dispatcher and the general kernel (the tiled kernels
-// are block_gemm_tile.hpp's), which takes any
-// layout, size, stride and alignment: every lane gathers its operand bytes
-// one by one and each wave owns a 16 x 16 output tile, whose 16x16x128
-// matrix instruction covers exactly one group of k.
+// This file holds the dispatcher and the general kernel, which takes any
+// layout, size, stride and alignment (the tiled kernels, for operands of
+// whole 16-byte pieces, are block_gemm_tile.hpp's).
 
 #include "block.hpp"
 #include "block_gemm_tile.hpp"
@@ -19,65 +17,203 @@ namespace fp8lin {
 
 namespace {
 
-constexpr int kGenThreads = 256;  // 4 waves, 2 x 2 grid of 16 x 16 tiles
+// The general kernel: two LDS stages of one group of k in the tiled kernels'
+// layout.  Operands come through registers: a lane's 16 bytes may begin at
+// any address (the vector memory unit takes unaligned ones); where the
+// matrix ends inside them, the row's last 16 are loaded and shifted down.
+// Two stages are in flight in registers while one is multiplied.  Both
+// operands' steps are per line here (a tile's is repeated), and all offsets
+// are 64-bit.
+template <bool MN, int R, int NW>
+struct AnyOperand {
+    using Op = Operand<MN, R, NW, kGroup>;
+    static constexpr int kPer = Op::kPerWave;
+    uint4 v[kPer];
 
-__device__ __forceinline__ float scale_at(const BlockScale& s, int64_t i, int64_t kb) {
-    return s.s[(i >> s.shift) * s.si + kb * s.sk];
-}
-
-template <int FA, int FB>
-__global__ __launch_bounds__(kGenThreads) void block_gemm_general_kernel(BlockGemmLaunch p) {
-    const int lane = threadIdx.x % kWave;
-    const int wave = threadIdx.x / kWave;
-    const int64_t col0 = (int64_t)blockIdx.x * 32 + (wave % 2) * 16;
-    const int64_t bc = col0 + lane % 16;  // this lane's column of B and of the output
-    const int kq = 32 * (lane / 16);
-    for (int64_t by = blockIdx.y; by * 32 < p.m; by += gridDim.y) {
-        const int64_t row0 = by * 32 + (wave / 2) * 16;
-        const int64_t ar = row0 + lane % 16;  // this lane's row of A
-        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t k0 = 0, kb = 0; k0 < p.k; k0 += kGroup, ++kb) {
-            union {
-                v8i v;
-                uint8_t b[32];
-            } xa, xb;
-#pragma unroll 4
-            for (int j = 0; j < 32; ++j) {
-                const int64_t kk = k0 + kq + j;
-                uint8_t va = 0, vb = 0;
-                if (kk < p.k) {
-                    if (ar < p.m) va = p.trans_a ? p.a[kk * p.lda + ar] : p.a[ar * p.lda + kk];
-                    if (bc < p.n) vb = p.trans_b ? p.b[bc * p.ldb + kk] : p.b[kk * p.ldb + bc];
-                }
-                xa.b[j] = va;
-                xb.b[j] = vb;
-            }
-            const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                xa.v, xb.v, v4f{0.0f, 0.0f, 0.0f, 0.0f}, FA, FB, 0, 0, 0, 0);
-            const float sb = bc < p.n ? scale_at(p.sb, bc, kb) : 0.0f;
+    // The stage at k0: `base` is the operand at this tile's first line.
+    __device__ void load(const uint8_t* base, int64_t ld, int64_t lines, int64_t k0, int64_t k,
+                         int wave, int lane) {
+        const int64_t rows = MN ? k : lines, width = MN ? lines : k;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t r = row0 + 4 * (lane / 16) + i;
-                const float sa = r < p.m ? scale_at(p.sa, r, kb) : 0.0f;
-                acc[i] = fmaf(part[i], sa * sb, acc[i]);
+        for (int j = 0; j < kPer; ++j) {
+            int row, c;
+            Op::slot(j, wave, lane, row, c);
+            const int64_t across = MN ? k0 + row : row;       // which stored row
+            const int64_t along = MN ? 16 * c : k0 + 16 * c;  // first byte in it
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (across >= rows || along >= width) continue;
+            const uint8_t* src = base + across * ld;
+            const int64_t over = along + 16 - width;  // bytes past the row's end
+            if (over <= 0) {
+                __builtin_memcpy(&v[j], src + along, 16);
+            } else if (width >= 16) {
+                uint64_t w[2];
+                __builtin_memcpy(w, src + width - 16, 16);
+                const int bits = 8 * (int)over;  // 8 .. 120
+                const uint64_t lo = bits < 64 ? w[0] >> bits | w[1] << (64 - bits)
+                                              : w[1] >> (bits - 64);
+                const uint64_t hi = bits < 64 ? w[1] >> bits : 0;
+                v[j] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
+                                  (uint32_t)(hi >> 32));
+            } else {  // the whole row is shorter
+                uint64_t w[2] = {0, 0};
+                for (int i = 0; i < width; ++i)
+                    w[i / 8] |= (uint64_t)src[along + i] << (8 * (i % 8));
+                v[j] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1],
+                                  (uint32_t)(w[1] >> 32));
             }
         }
-        if (bc >= p.n) continue;
-        const float bias = p.bias ? bf16_to_f32(p.bias[bc]) : 0.0f;
+    }
+    __device__ void store(uint8_t* lds, int wave, int lane) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = row0 + 4 * (lane / 16) + i;
-            if (r < p.m) p.out[r * p.n + bc] = f32_to_bf16(acc[i] + bias);
+        for (int j = 0; j < kPer; ++j)
+            *reinterpret_cast<uint4*>(lds + 1024 * (wave + j * NW) + 16 * lane) = v[j];
+    }
+};
+
+template <int FA, int FB, bool AMN, bool BMN, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64) void block_gemm_general_kernel(BlockGemmLaunch p,
+                                                                        int64_t tiles,
+                                                                        int64_t tiles_n) {
+    constexpr int kStage = (BM + BN) * kGroup + 4 * (BM + BN);
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+    constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FN = TN / 32;
+    static_assert(TM == 32, "one row tile per wave");
+    static_assert(BM + BN <= NW * 64, "a step per lane");
+    using OA = AnyOperand<AMN, BM, NW>;
+    using OB = AnyOperand<BMN, BN, NW>;
+    constexpr int kRowA = AMN ? 0 : kGroup, kRowB = BMN ? 0 : kGroup;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t groups = (p.k + kGroup - 1) / kGroup;
+    const uint32_t aoff = OA::Op::frag_off(AMN ? wm * TM : 0, lane);
+    uint32_t boff[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) boff[j] = OB::Op::frag_off(BMN ? wn * TN + 32 * j : 0, lane);
+
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t m0 = tile / tiles_n * BM, n0 = tile % tiles_n * BN;
+        const uint8_t* a = p.a + (AMN ? m0 : m0 * p.lda);
+        const uint8_t* b = p.b + (BMN ? n0 : n0 * p.ldb);
+        // lane e carries a step: row e's, then column e - BM's
+        const int e = threadIdx.x;
+        const float* step = nullptr;
+        int64_t step_k = 0;
+        if (e < BM && m0 + e < p.m) {
+            step = p.sa.s + ((m0 + e) >> p.sa.shift) * p.sa.si;
+            step_k = p.sa.sk;
+        } else if (e >= BM && e < BM + BN && n0 + e - BM < p.n) {
+            step = p.sb.s + ((n0 + e - BM) >> p.sb.shift) * p.sb.si;
+            step_k = p.sb.sk;
+        }
+        struct Stage {
+            OA a;
+            OB b;
+            float s = 0.0f;
+        } one, two;
+        auto load = [&](Stage& v, int64_t g) __attribute__((always_inline)) {
+            if (g >= groups) return;
+            v.a.load(a, p.lda, p.m - m0, g * kGroup, p.k, wave, lane);
+            v.b.load(b, p.ldb, p.n - n0, g * kGroup, p.k, wave, lane);
+            if (step) v.s = step[g * step_k];
+        };
+        auto store = [&](const Stage& v, int64_t g) __attribute__((always_inline)) {
+            if (g >= groups) return;
+            uint8_t* at = smem + (g & 1) * kStage;
+            v.a.store(at, wave, lane);
+            v.b.store(at + BM * kGroup, wave, lane);
+            if (e < BM + BN) *reinterpret_cast<float*>(at + (BM + BN) * kGroup + 4 * e) = v.s;
+        };
+        v16f acc[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][i] = 0.0f;
+        auto multiply = [&](int64_t g) __attribute__((always_inline)) {
+            uint8_t* at = smem + (g & 1) * kStage;
+            const uint8_t* la = at + wm * TM * kRowA;
+            const uint8_t* lb = at + BM * kGroup + wn * TN * kRowB;
+            const float* ls = reinterpret_cast<const float*>(at + (BM + BN) * kGroup);
+            const v8i a0 = OA::Op::template frag<0>(la, aoff);
+            const v8i a1 = OA::Op::template frag<1>(la, aoff);
+            const float sa = ls[wm * TM + (lane & 31)];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                v16f part = {0};
+                part = mfma_ba<FA, FB>(OB::Op::template frag<0>(lb + 32 * j * kRowB, boff[j]), a0,
+                                       part);
+                part = mfma_ba<FA, FB>(OB::Op::template frag<1>(lb + 32 * j * kRowB, boff[j]), a1,
+                                       part);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v4f sb = *reinterpret_cast<const v4f*>(
+                        ls + BM + wn * TN + 32 * j + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[j][4 * q + i] = fmaf(part[4 * q + i] * sa, sb[i], acc[j][4 * q + i]);
+                }
+            }
+        };
+        // Stage g is in LDS, g + 1 in `next` and g + 2 on its way: `next` goes
+        // to the slot that stage g - 1 left before the last barrier.
+        auto turn = [&](Stage& next, int64_t g) __attribute__((always_inline)) {
+            store(next, g + 1);
+            load(next, g + 3);
+            multiply(g);
+            __syncthreads();
+        };
+        load(one, 0);
+        load(two, 1);
+        store(one, 0);
+        load(one, 2);
+        __syncthreads();
+        for (int64_t g = 0; g < groups; g += 2) {
+            turn(two, g);
+            if (g + 1 < groups) turn(one, g + 1);
+        }
+        // acc[j][e] is row m0 + wm*TM + lane%32, column n0 + wn*TN + 32j +
+        // 8*(e/4) + 4*(lane/32) + e%4
+        const int64_t gm = m0 + wm * TM + (lane & 31);
+        if (gm < p.m) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int64_t gn =
+                        n0 + wn * TN + 32 * j + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+                    if (gn < p.n) {
+                        const float bias = p.bias ? bf16_to_f32(p.bias[gn]) : 0.0f;
+                        p.out[gm * p.n + gn] = f32_to_bf16(acc[j][i] + bias);
+                    }
+                }
         }
     }
 }
 
+template <int FA, int FB, bool AMN, bool BMN>
+hipError_t launch_general_layout(const BlockGemmLaunch& g, hipStream_t stream) {
+    auto tiles = [&](int s) { return (g.m + s - 1) / s * ((g.n + s - 1) / s); };
+    auto grid = [](int64_t t) { return dim3((unsigned)(t < (1 << 20) ? t : 1 << 20)); };
+    // 128 x 128 tiles read half the operand bytes per output that 64 x 64 ones
+    // do, once there are enough of them for every CU.
+    if (tiles(128) >= 256)
+        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 128, 128, 4, 2>),
+                           grid(tiles(128)), dim3(512), 0, stream, g, tiles(128),
+                           (g.n + 127) / 128);
+    else
+        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 64, 64, 2, 2>),
+                           grid(tiles(64)), dim3(256), 0, stream, g, tiles(64), (g.n + 63) / 64);
+    return hipGetLastError();
+}
+
 template <int FA, int FB>
 hipError_t launch_general(const BlockGemmLaunch& g, hipStream_t stream) {
-    const int64_t gy = (g.m + 31) / 32;
-    const dim3 grid((unsigned)((g.n + 31) / 32), (unsigned)(gy < 65535 ? gy : 65535));
-    hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB>), grid, dim3(kGenThreads), 0, stream, g);
-    return hipGetLastError();
+    const bool am = g.trans_a != 0, bm = g.trans_b == 0;
+    if (am) return bm ? launch_general_layout<FA, FB, true, true>(g, stream)
+                      : launch_general_layout<FA, FB, true, false>(g, stream);
+    return bm ? launch_general_layout<FA, FB, false, true>(g, stream)
+              : launch_general_layout<FA, FB, false, false>(g, stream);
 }
 
 }  // namespace

@@ -38,8 +38,8 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxExperts = 512, kMaxTokens = 1024;
 constexpr int kRouteTokens = 4;   // tokens of a routing workgroup
 constexpr int kTiles = 4;         // 16-row tiles of weights per wave
-constexpr int kUnits = 32;        // hidden units of a gate / up workgroup
-constexpr int kRows = 64;         // rows of W2 of a down workgroup
+constexpr int kUnits = 8 * kTiles;        // hidden units of a gate / up workgroup
+constexpr int kRows = 16 * kTiles;         // rows of W2 of a down workgroup
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -372,33 +372,40 @@ __device__ __forceinline__ bf16x8 as_bf16(const uint4& v) {
 // 128-k blocks wave, wave + 4, ... of `kdim`: acc[tile] += step * sum.
 // Lane l holds rows l % 16 and k = 64 i + 16 (l / 16) .. + 15 of a block (i =
 // 0, 1) on both sides, which is a reordering of k that the sum does not see.
-//   w[tile]: this lane's row at its first k;  s[tile]: the tile's steps.
-//   act[ACT]: the token's activations (added: the lane's rest, if any).
+//   w[tile]: the tile's first row;  s[tile]: its steps (both uniform).
+//   act[ACT]: activations, of which this lane's token's begin at element
+//   `at` (the second ones are added: what the first's rounding left).
 template <int FMT, int ACT>
 __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
                                               const float* const (&s)[kTiles],
-                                              const uint16_t* const (&act)[ACT], int kdim,
-                                              int wave, int lane, v4f (&acc)[kTiles]) {
+                                              const uint16_t* const (&act)[ACT], uint32_t at,
+                                              int kdim, int wave, int lane,
+                                              v4f (&acc)[kTiles]) {
     const int kq = 16 * (lane / 16);
+    const uint32_t wo = (uint32_t)((lane % 16) * kdim + kq);
+    const uint32_t xo = 2 * (at + kq);
+    auto load16 = [](const void* base, uint32_t offset) __attribute__((always_inline)) {
+        return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + offset);
+    };
     struct Block {
         uint4 w[kTiles][2];
         uint4 x[ACT][2][2];
         float s[kTiles];
     };
-    auto load = [&](int b, Block& k) __attribute__((always_inline)) {
-        const bool whole = kGroup * (b + 1) <= kdim;  // uniform
+    auto load = [&](int n, Block& b) __attribute__((always_inline)) {
+        const bool whole = kGroup * (n + 1) <= kdim;  // uniform
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int k0 = kGroup * b + 64 * i;
+            const int k0 = kGroup * n + 64 * i;
             // kdim is a multiple of 16: a lane's 16 k exist or none does
             const bool in = whole || k0 + kq < kdim;
-            const int at = in ? k0 : -kq;  // (one that exists instead)
+            const int k = in ? k0 : -kq;  // (one that exists instead)
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) k.w[t][i] = *reinterpret_cast<const uint4*>(w[t] + at);
+            for (int t = 0; t < kTiles; ++t) b.w[t][i] = load16(w[t], wo + k);
 #pragma unroll
             for (int a = 0; a < ACT; ++a) {
-                k.x[a][i][0] = *reinterpret_cast<const uint4*>(act[a] + at);
-                k.x[a][i][1] = *reinterpret_cast<const uint4*>(act[a] + at + 8);
+                b.x[a][i][0] = load16(act[a], xo + 2 * k);
+                b.x[a][i][1] = load16(act[a], xo + 2 * k + 16);
             }
             if (!whole) {
                 auto keep = [&](uint4& v) __attribute__((always_inline)) {
@@ -408,13 +415,13 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
                     v.w = in ? v.w : 0u;
                 };
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) keep(k.w[t][i]);
+                for (int t = 0; t < kTiles; ++t) keep(b.w[t][i]);
 #pragma unroll
-                for (int a = 0; a < ACT; ++a) keep(k.x[a][i][0]), keep(k.x[a][i][1]);
+                for (int a = 0; a < ACT; ++a) keep(b.x[a][i][0]), keep(b.x[a][i][1]);
             }
         }
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) k.s[t] = s[t][b];
+        for (int t = 0; t < kTiles; ++t) b.s[t] = s[t][n];
     };
     auto multiply = [&](const Block& k) __attribute__((always_inline)) {
 #pragma unroll
@@ -478,33 +485,33 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int f0 = blockIdx.x * kUnits;
     const int kg = (p.dim + kGroup - 1) / kGroup, rg = (2 * p.hidden + kGroup - 1) / kGroup;
-    const uint8_t* w[kTiles];  // gate, gate, up, up
+    constexpr int kHalf = kTiles / 2;  // tiles of gate rows, then as many of up rows
+    const uint8_t* w[kTiles];
     const float* s[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         // 16 rows share a tile of steps (hidden is a multiple of 16); a second
         // 16 units past the last repeat the first
-        const int f = f0 + 16 * (t % 2) < p.hidden ? f0 + 16 * (t % 2) : f0;
-        const int row = f + t / 2 * p.hidden;
-        w[t] = p.w13 + (e * 2 * p.hidden + row + lane % 16) * p.dim + 16 * (lane / 16);
+        const int f = f0 + 16 * (t % kHalf) < p.hidden ? f0 + 16 * (t % kHalf) : f0;
+        const int row = f + t / kHalf * p.hidden;
+        w[t] = p.w13 + (e * 2 * p.hidden + row) * p.dim;
         s[t] = p.s13 + (e * rg + row / kGroup) * kg;
     }
     for (int c0 = 0; c0 < work.count; c0 += 16) {
         // lanes past the list repeat its last token; their results are dropped
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
         const int slot = ws.slots[work.first + c];
-        const uint16_t* const x[1] = {p.x + (int64_t)(slot / p.top_k) * p.dim +
-                                      16 * (lane / 16)};
+        const uint16_t* const x[1] = {p.x};
         v4f acc[kTiles] = {};
-        tile_products<FMT, 1>(w, s, x, p.dim, wave, lane, acc);
+        tile_products<FMT, 1>(w, s, x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave, lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
             const int64_t o = (int64_t)ws.slots[work.first + c0 + tid / 16] * p.hidden + f0 +
                               tid % 16;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float h = v[i] / (1.0f + expf(-v[i])) * v[2 + i];
+            for (int i = 0; i < kHalf; ++i) {
+                const float h = v[i] / (1.0f + expf(-v[i])) * v[kHalf + i];
                 const uint16_t hi = f32_to_bf16(h);
                 if (f0 + 16 * i < p.hidden) {
                     ws.h_hi[o + 16 * i] = hi;
@@ -536,15 +543,15 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs w
     for (int t = 0; t < kTiles; ++t) {
         // dim is a multiple of 16: a tile past it repeats the first
         const int row = d0 + 16 * t < p.dim ? d0 + 16 * t : d0;
-        w[t] = p.w2 + (e * p.dim + row + lane % 16) * p.hidden + 16 * (lane / 16);
+        w[t] = p.w2 + (e * p.dim + row) * p.hidden;
         s[t] = p.s2 + (e * rg + row / kGroup) * kg;
     }
     for (int c0 = 0; c0 < work.count; c0 += 16) {
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
-        const int64_t at = (int64_t)ws.slots[work.first + c] * p.hidden + 16 * (lane / 16);
-        const uint16_t* const h[2] = {ws.h_hi + at, ws.h_lo + at};
+        const uint32_t at = (uint32_t)(ws.slots[work.first + c] * p.hidden);
+        const uint16_t* const h[2] = {ws.h_hi, ws.h_lo};
         v4f acc[kTiles] = {};
-        tile_products<FMT, 2>(w, s, h, p.hidden, wave, lane, acc);
+        tile_products<FMT, 2>(w, s, h, at, p.hidden, wave, lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
