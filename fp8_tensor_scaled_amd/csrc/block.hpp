@@ -23,8 +23,15 @@ struct BlockQuantLaunch {
     float* scale_col = nullptr;   // [groups_of(rows)][cols]
     uint8_t* out_tile = nullptr;  // [rows][cols]
     float* scale_tile = nullptr;  // [groups_of(rows)][groups_of(cols)]
+    // With row and col of a bf16 input: receives the sums of each 128 rows of
+    // each column, [groups_of(rows)][cols] (the bias gradient's partials).
+    float* sums = nullptr;
 };
 hipError_t launch_quantize_block(const BlockQuantLaunch& q, hipStream_t stream);
+// Two bf16 quantizes of one format in one launch: x by rows (and columns),
+// w by tiles; the results are those of two launches.
+hipError_t launch_quantize_block_two(const BlockQuantLaunch& x, const BlockQuantLaunch& w,
+                                     hipStream_t stream);
 
 // Where the step of output row i (or column j) and k group kb lies:
 // scale[(i >> shift) * si + kb * sk].

@@ -5,14 +5,23 @@
 // (The step takes one multiplication where the per-tensor ring's fold takes a
 // division, once per tensor: the two can differ in the last bit.)
 //
-// One workgroup of 256 lanes holds one 128 x 128 tile of x in registers
-// (lane t: columns 8 (t % 16) .. +7 of rows t / 16 + 16 i), so x is read
-// once whatever is asked: a row group's maximum is that of 16 neighbouring
-// lanes, a column group's that of a lane's own 8 rows, of the 4 row lanes of
-// its wave and, through LDS, of the 4 waves.  16 lanes read 256 bytes of a
-// row (bf16) and write the 128 bytes of its codes: whole lines both ways.
-// Memory bound: 3 bytes per element for one grouping of a 2-byte input, 4
-// for both.
+// A workgroup of T lanes holds a band of 128 columns in registers (lane t:
+// columns 8 (t % 16) .. +7 of rows t / 16 + (T / 16) i, i < P; 128 rows
+// where columns or tiles are grouped), so x is read once whatever is asked.  A
+// row group's maximum is that of 16 neighbouring lanes; a column group's that
+// of a lane's own rows, of the 4 row lanes of its wave and, through LDS, of
+// the waves.  16 lanes read 256 bytes of a row (2-byte inputs) and write the
+// 128 bytes of its codes: whole lines both ways.  Each reciprocal (a
+// correctly rounded division) is taken by one lane and handed to the others.
+//
+// Without a margin nothing has to be clamped before the conversion: |x| <=
+// max |x| gives |x / s| <= FMAX (1 + 2^-22), which rounds to FMAX at most, and
+// a larger step only lowers it.
+//
+// Memory bound when large (3 bytes per element for one grouping of a 2-byte
+// input, 4 for both); a few tiles are bound by the chain of one tile (load,
+// maxima, division, conversion), so there 1024 lanes share a tile instead of
+// 256 (see launch_kinds).
 
 #include "block.hpp"
 #include "common.hpp"
@@ -21,14 +30,9 @@ namespace fp8lin {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRowsPer = kThreads / 16;       // rows a pass of the workgroup covers
-constexpr int kPasses = kGroup / kRowsPer;    // 8 rows per lane
-
 struct BlockQuantParams {
     const void* x;
     int64_t rows, cols, ldx;
-    int fmt;
     float rmargin;  // 2^-margin
     uint8_t* out_row;
     float* scale_row;
@@ -36,6 +40,7 @@ struct BlockQuantParams {
     float* scale_col;
     uint8_t* out_tile;
     float* scale_tile;
+    float* sums;  // [groups_of(rows)][cols] column sums of x over each 128 rows
     int64_t col_groups;
     int vec_out;  // codes go out 8 at a time: cols % 8 == 0 and aligned outputs
 };
@@ -63,6 +68,20 @@ __device__ __forceinline__ float step_of(float amax, float rfmax, float rmargin)
     return fmaxf(amax * rfmax * rmargin, 1e-12f);
 }
 
+// Four codes, without a clamp.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    int w;
+    if constexpr (FMT) {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    }
+    return (uint32_t)w;
+}
+
 // Eight codes of one row: columns c .. c + 7, those past cols dropped.
 __device__ __forceinline__ void store8(uint8_t* out, int64_t row, int64_t c, int64_t cols,
                                        int vec, uint32_t lo, uint32_t hi) {
@@ -71,160 +90,244 @@ __device__ __forceinline__ void store8(uint8_t* out, int64_t row, int64_t c, int
         *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
         return;
     }
+    if (c + 8 <= cols) {
+        const uint2 w = make_uint2(lo, hi);
+        __builtin_memcpy(dst, &w, 8);
+        return;
+    }
     const uint64_t w = lo | (uint64_t)hi << 32;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (c + j < cols) dst[j] = (uint8_t)(w >> (8 * j));
 }
 
-template <int IN, bool ROW, bool COL, bool TILE>
-__global__ __launch_bounds__(kThreads) void quantize_block_kernel(BlockQuantParams p) {
+// This lane's value from lane (its row of 16's first + N).
+template <int N>
+__device__ __forceinline__ float from_lane16(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + N, 0xf, 0xf,
+                                                      false));  // row_newbcast:N
+}
+template <int N>
+__device__ __forceinline__ float rotate16(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf,
+                                                      false));  // row_ror:N
+}
+// op over the 16 lanes of a row, in every lane.
+template <class Op>
+__device__ __forceinline__ float all16(float v, Op op) {
+    v = op(v, rotate16<8>(v));
+    v = op(v, rotate16<4>(v));
+    v = op(v, rotate16<2>(v));
+    return op(v, rotate16<1>(v));
+}
+// op over lanes l, l ^ 16, l ^ 32, l ^ 48, in every lane.
+template <class Op>
+__device__ __forceinline__ float across_rows(float v, Op op) {
+    const int a = __float_as_int(v);
+    const auto s = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = op(__int_as_float(s[0]), __int_as_float(s[1]));
+    const int b = __float_as_int(v);
+    const auto t = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return op(__int_as_float(t[0]), __int_as_float(t[1]));
+}
+
+// 16 bytes at any element's address.
+typedef uint32_t AnyVec4 __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int T>
+struct QuantLds {
+    float red[T / kWave][kGroup];
+    float sum[T / kWave][kGroup];
+    float inv[kGroup];
+};
+
+// The band of 128 columns of column group cg and the T / 16 * P rows from
+// row r_first (with COL, TILE or SUM: the 128 rows of row group rg).
+template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM, int T, int P>
+__device__ __forceinline__ void quantize_band(const BlockQuantParams& p, int64_t cg, int64_t rg,
+                                              QuantLds<T>& lds) {
     using E = Elem<IN>;
-    using T = typename E::T;
-    __shared__ float red[4][kGroup];
+    using V = typename E::T;
+    constexpr int kRowsPer = T / 16, NW = T / kWave;
+    static_assert(!(COL || TILE || SUM) || kRowsPer * P == kGroup, "a whole group of rows");
+    constexpr float rfmax = 1.0f / fmt_max<FMT>();
+    auto max2 = [](float a, float b) { return fmaxf(a, b); };
+    auto add2 = [](float a, float b) { return a + b; };
     const int tid = threadIdx.x;
     const int wave = tid / kWave;
     const int cl = 8 * (tid % 16);
-    const int64_t cg = (int64_t)blockIdx.x % p.col_groups, rg = (int64_t)blockIdx.x / p.col_groups;
     const int64_t c = cg * kGroup + cl;
-    const int64_t r0 = rg * kGroup + tid / 16;
-    const float rfmax = p.fmt ? 1.0f / fmt_max<1>() : 1.0f / fmt_max<0>();
-    const T* x = static_cast<const T*>(p.x);
+    const int64_t r0 = rg * (kRowsPer * P) + tid / 16;
+    const V* x = static_cast<const V*>(p.x);
 
-    T raw[kPasses][8];
+    V raw[P][8];
+    constexpr int kLoads = (int)sizeof(V) * 8 / 16;  // 16-byte loads of a row
+    AnyVec4 v[P][kLoads];
     const bool whole = c + 8 <= p.cols;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < P; ++i) {
         const int64_t r = r0 + kRowsPer * i;
-        const T* src = x + r * p.ldx + c;
+        const V* src = x + r * p.ldx + c;
         if (r < p.rows && whole) {
-            __builtin_memcpy(raw[i], src, sizeof raw[i]);
+            // read once: past the caches (8192 x 8192 bf16 tiles 35 us, 51 without;
+            // fp32 58 either way)
+#pragma unroll
+            for (int z = 0; z < kLoads; ++z)
+                v[i][z] = __builtin_nontemporal_load(reinterpret_cast<const AnyVec4*>(src) + z);
+            __builtin_memcpy(raw[i], v[i], sizeof raw[i]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) raw[i][j] = r < p.rows && c + j < p.cols ? src[j] : T(0);
+            for (int j = 0; j < 8; ++j) raw[i][j] = r < p.rows && c + j < p.cols ? src[j] : V(0);
         }
     }
 
-    float rmax[kPasses];
-    float cmax[8];
+    float rmax[P], cmax[8], csum[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) cmax[j] = csum[j] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < P; ++i) {
         rmax[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = fabsf(E::f(raw[i][j]));  // (fmaxf drops NaN)
-            rmax[i] = fmaxf(rmax[i], v);
-            if constexpr (COL) cmax[j] = fmaxf(cmax[j], v);
+            const float v = E::f(raw[i][j]);
+            if constexpr (ROW || TILE) rmax[i] = fmaxf(rmax[i], fabsf(v));  // (drops NaN)
+            if constexpr (COL) cmax[j] = fmaxf(cmax[j], fabsf(v));
+            if constexpr (SUM) csum[j] += v;
         }
     }
-
-    // codes of pass i with the reciprocals m (one per column)
-    auto encode = [&](int i, const float (&m)[8], uint32_t& lo, uint32_t& hi) {
-        lo = cvt4_rt(p.fmt, E::f(raw[i][0]) * m[0], E::f(raw[i][1]) * m[1],
-                     E::f(raw[i][2]) * m[2], E::f(raw[i][3]) * m[3]);
-        hi = cvt4_rt(p.fmt, E::f(raw[i][4]) * m[4], E::f(raw[i][5]) * m[5],
-                     E::f(raw[i][6]) * m[6], E::f(raw[i][7]) * m[7]);
+    // codes of row i with the reciprocals m (one per column)
+    auto write = [&](uint8_t* out, int i, const float (&m)[8]) __attribute__((always_inline)) {
+        const int64_t r = r0 + kRowsPer * i;
+        if (r >= p.rows || c >= p.cols) return;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = E::f(raw[i][j]) * m[j];
+        if (p.rmargin != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = sat<FMT>(v[j]);
+        }
+        store8(out, r, c, p.cols, p.vec_out, encode4<FMT>(v[0], v[1], v[2], v[3]),
+               encode4<FMT>(v[4], v[5], v[6], v[7]));
     };
 
-    if constexpr (ROW) {
+    if constexpr (COL || SUM) {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            float a = rmax[i];
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (COL) cmax[j] = across_rows(cmax[j], max2);
+            if constexpr (SUM) csum[j] = across_rows(csum[j], add2);
+        }
+        if (tid % kWave < 16) {
 #pragma unroll
-            for (int off = 8; off >= 1; off >>= 1) a = fmaxf(a, __shfl_xor(a, off, kWave));
-            const float s = step_of(a, rfmax, p.rmargin);
-            const float inv = __fdiv_rn(1.0f, s);
-            const float m[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
-            const int64_t r = r0 + kRowsPer * i;
-            if (r < p.rows && c < p.cols) {
-                uint32_t lo, hi;
-                encode(i, m, lo, hi);
-                store8(p.out_row, r, c, p.cols, p.vec_out, lo, hi);
-                if (cl == 0) p.scale_row[r * p.col_groups + cg] = s;
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (COL) lds.red[wave][cl + j] = cmax[j];
+                if constexpr (SUM) lds.sum[wave][cl + j] = csum[j];
             }
+        }
+        __syncthreads();
+        if (tid < kGroup) {
+            const int64_t col = cg * kGroup + tid;
+            if constexpr (COL) {
+                float a = lds.red[0][tid];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) a = fmaxf(a, lds.red[w][tid]);
+                const float s = step_of(a, rfmax, p.rmargin);
+                lds.inv[tid] = __fdiv_rn(1.0f, s);
+                if (col < p.cols) p.scale_col[rg * p.cols + col] = s;
+            }
+            if constexpr (SUM) {
+                float a = lds.sum[0][tid];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) a += lds.sum[w][tid];
+                if (col < p.cols) p.sums[rg * p.cols + col] = a;
+            }
+        }
+        if constexpr (COL) __syncthreads();
+    }
+    if constexpr (ROW) {
+        float inv[P];
+        // lane i of a row of 16 divides for row i, all of them for few rows
+        float mine = 0.0f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            rmax[i] = all16(rmax[i], max2);
+            mine = tid % 16 == i || P == 1 ? rmax[i] : mine;
+        }
+        const float s = step_of(mine, rfmax, p.rmargin);
+        const float r1 = __fdiv_rn(1.0f, s);
+        inv[0] = from_lane16<0>(r1);
+        if constexpr (P > 1) inv[1] = from_lane16<1>(r1);
+        if constexpr (P > 2) {
+            static_assert(P <= 2 || P == 8, "rows per lane");
+            inv[2] = from_lane16<2>(r1);
+            inv[3] = from_lane16<3>(r1);
+            inv[4] = from_lane16<4>(r1);
+            inv[5] = from_lane16<5>(r1);
+            inv[6] = from_lane16<6>(r1);
+            inv[7] = from_lane16<7>(r1);
+        }
+        if (tid % 16 < P) {
+            const int64_t r = r0 + kRowsPer * (tid % 16);
+            if (r < p.rows) p.scale_row[r * p.col_groups + cg] = s;
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float m[8] = {inv[i], inv[i], inv[i], inv[i], inv[i], inv[i], inv[i], inv[i]};
+            write(p.out_row, i, m);
         }
     }
     if constexpr (COL) {
+        float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float a = cmax[j];
-            a = fmaxf(a, __shfl_xor(a, 16, kWave));
-            a = fmaxf(a, __shfl_xor(a, 32, kWave));
-            if (tid % kWave < 16) red[wave][cl + j] = a;
-        }
-        __syncthreads();
-        float m[8], s[8];
+        for (int j = 0; j < 8; ++j) m[j] = lds.inv[cl + j];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = fmaxf(fmaxf(red[0][cl + j], red[1][cl + j]),
-                                  fmaxf(red[2][cl + j], red[3][cl + j]));
-            s[j] = step_of(a, rfmax, p.rmargin);
-            m[j] = __fdiv_rn(1.0f, s[j]);
-        }
-        if (tid < 16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < p.cols) p.scale_col[rg * p.cols + c + j] = s[j];
-        }
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int64_t r = r0 + kRowsPer * i;
-            if (r < p.rows && c < p.cols) {
-                uint32_t lo, hi;
-                encode(i, m, lo, hi);
-                store8(p.out_col, r, c, p.cols, p.vec_out, lo, hi);
-            }
-        }
+        for (int i = 0; i < P; ++i) write(p.out_col, i, m);
     }
     if constexpr (TILE) {
-        float a = 0.0f;
+        float a = rmax[0];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) a = fmaxf(a, rmax[i]);
-        a = wave_max(a);
-        if (tid % kWave == 0) red[0][wave] = a;
+        for (int i = 1; i < P; ++i) a = fmaxf(a, rmax[i]);
+        a = across_rows(all16(a, max2), max2);
+        if (tid % kWave == 0) lds.red[0][wave] = a;
         __syncthreads();
-        a = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+#pragma unroll
+        for (int w = 0; w < NW; ++w) a = fmaxf(a, lds.red[0][w]);
         const float s = step_of(a, rfmax, p.rmargin);
-        const float inv = __fdiv_rn(1.0f, s);
-        const float m[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
+        const float r1 = __fdiv_rn(1.0f, s);
+        const float m[8] = {r1, r1, r1, r1, r1, r1, r1, r1};
         if (tid == 0) p.scale_tile[rg * p.col_groups + cg] = s;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int64_t r = r0 + kRowsPer * i;
-            if (r < p.rows && c < p.cols) {
-                uint32_t lo, hi;
-                encode(i, m, lo, hi);
-                store8(p.out_tile, r, c, p.cols, p.vec_out, lo, hi);
-            }
-        }
+        for (int i = 0; i < P; ++i) write(p.out_tile, i, m);
     }
 }
 
-template <int IN>
-hipError_t launch_in(const BlockQuantParams& p, int64_t grid, hipStream_t stream) {
-    const dim3 g((unsigned)grid), b(kThreads);
-    if (p.out_tile)
-        hipLaunchKernelGGL((quantize_block_kernel<IN, false, false, true>), g, b, 0, stream, p);
-    else if (p.out_row && p.out_col)
-        hipLaunchKernelGGL((quantize_block_kernel<IN, true, true, false>), g, b, 0, stream, p);
-    else if (p.out_row)
-        hipLaunchKernelGGL((quantize_block_kernel<IN, true, false, false>), g, b, 0, stream, p);
-    else
-        hipLaunchKernelGGL((quantize_block_kernel<IN, false, true, false>), g, b, 0, stream, p);
-    return hipGetLastError();
+template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM, int T, int P>
+__global__ __launch_bounds__(T) void quantize_block_kernel(BlockQuantParams p) {
+    __shared__ QuantLds<T> lds;
+    quantize_band<IN, FMT, ROW, COL, TILE, SUM, T, P>(
+        p, (int64_t)blockIdx.x % p.col_groups, (int64_t)blockIdx.x / p.col_groups, lds);
 }
 
-}  // namespace
+// The layer's forward: x by rows (and columns, WITH_COL) and w by tiles in
+// one launch, x's bands first.
+template <int FMT, bool WITH_COL, int T, int P>
+__global__ __launch_bounds__(T) void quantize_block_two_kernel(BlockQuantParams px,
+                                                              BlockQuantParams pw, int nx) {
+    __shared__ QuantLds<T> lds;
+    if ((int)blockIdx.x < nx)
+        quantize_band<kInBf16, FMT, true, WITH_COL, false, false, T, P>(
+            px, (int64_t)blockIdx.x % px.col_groups, (int64_t)blockIdx.x / px.col_groups, lds);
+    else
+        quantize_band<kInBf16, FMT, false, false, true, false, T, P>(
+            pw, (int64_t)(blockIdx.x - nx) % pw.col_groups,
+            (int64_t)(blockIdx.x - nx) / pw.col_groups, lds);
+}
 
-hipError_t launch_quantize_block(const BlockQuantLaunch& q, hipStream_t stream) {
+BlockQuantParams params_of(const BlockQuantLaunch& q) {
     BlockQuantParams p{};
     p.x = q.x;
     p.rows = q.rows;
     p.cols = q.cols;
     p.ldx = q.ldx;
-    p.fmt = q.fmt;
     p.rmargin = q.rmargin;
     p.out_row = q.out_row;
     p.scale_row = q.scale_row;
@@ -232,17 +335,81 @@ hipError_t launch_quantize_block(const BlockQuantLaunch& q, hipStream_t stream) 
     p.scale_col = q.scale_col;
     p.out_tile = q.out_tile;
     p.scale_tile = q.scale_tile;
+    p.sums = q.sums;
     p.col_groups = groups_of(q.cols);
     const uintptr_t outs = reinterpret_cast<uintptr_t>(q.out_row) |
                            reinterpret_cast<uintptr_t>(q.out_col) |
                            reinterpret_cast<uintptr_t>(q.out_tile);
     p.vec_out = q.cols % 8 == 0 && (outs & 7) == 0;
-    const int64_t grid = groups_of(q.rows) * p.col_groups;
-    switch (q.in_type) {
-        case kInBf16: return launch_in<kInBf16>(p, grid, stream);
-        case kInF16: return launch_in<kInF16>(p, grid, stream);
-        default: return launch_in<kInF32>(p, grid, stream);
+    return p;
+}
+
+// 1024 lanes a tile below this many tiles, 256 from it on.
+constexpr int64_t kManyTiles = 512;
+
+template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM>
+hipError_t launch_kinds(const BlockQuantParams& p, hipStream_t stream) {
+    const int64_t tiles = groups_of(p.rows) * p.col_groups;
+    if constexpr (ROW && !COL && !SUM) {
+        // rows alone need no 128-row span: 16 rows a workgroup, until 128 fill the chip
+        if (tiles < kManyTiles)
+            hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, true, false, false, false, 256, 1>),
+                               dim3((unsigned)((p.rows + 15) / 16 * p.col_groups)), dim3(256), 0,
+                               stream, p);
+        else
+            hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, true, false, false, false, 256, 8>),
+                               dim3((unsigned)tiles), dim3(256), 0, stream, p);
+    } else if (tiles < kManyTiles) {
+        hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, ROW, COL, TILE, SUM, 1024, 2>),
+                           dim3((unsigned)tiles), dim3(1024), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, ROW, COL, TILE, SUM, 256, 8>),
+                           dim3((unsigned)tiles), dim3(256), 0, stream, p);
     }
+    return hipGetLastError();
+}
+
+template <int IN, int FMT>
+hipError_t launch_in(const BlockQuantParams& p, hipStream_t stream) {
+    if (p.out_tile) return launch_kinds<IN, FMT, false, false, true, false>(p, stream);
+    if constexpr (IN == kInBf16) {
+        if (p.sums) return launch_kinds<IN, FMT, true, true, false, true>(p, stream);
+    }
+    if (p.out_row && p.out_col) return launch_kinds<IN, FMT, true, true, false, false>(p, stream);
+    if (p.out_row) return launch_kinds<IN, FMT, true, false, false, false>(p, stream);
+    return launch_kinds<IN, FMT, false, true, false, false>(p, stream);
+}
+
+template <int FMT, bool WITH_COL>
+hipError_t launch_two(const BlockQuantParams& px, const BlockQuantParams& pw, hipStream_t stream) {
+    const int64_t nx = groups_of(px.rows) * px.col_groups;
+    const int64_t nw = groups_of(pw.rows) * pw.col_groups;
+    const dim3 grid((unsigned)(nx + nw));
+    if (nx + nw < kManyTiles)
+        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 1024, 2>), grid, dim3(1024), 0,
+                           stream, px, pw, (int)nx);
+    else
+        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 256, 8>), grid, dim3(256), 0,
+                           stream, px, pw, (int)nx);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_block(const BlockQuantLaunch& q, hipStream_t stream) {
+    const BlockQuantParams p = params_of(q);
+    switch (q.in_type) {
+        case kInBf16: return q.fmt ? launch_in<kInBf16, 1>(p, stream) : launch_in<kInBf16, 0>(p, stream);
+        case kInF16: return q.fmt ? launch_in<kInF16, 1>(p, stream) : launch_in<kInF16, 0>(p, stream);
+        default: return q.fmt ? launch_in<kInF32, 1>(p, stream) : launch_in<kInF32, 0>(p, stream);
+    }
+}
+
+hipError_t launch_quantize_block_two(const BlockQuantLaunch& x, const BlockQuantLaunch& w,
+                                     hipStream_t stream) {
+    const BlockQuantParams px = params_of(x), pw = params_of(w);
+    if (x.fmt) return x.out_col ? launch_two<1, true>(px, pw, stream) : launch_two<1, false>(px, pw, stream);
+    return x.out_col ? launch_two<0, true>(px, pw, stream) : launch_two<0, false>(px, pw, stream);
 }
 
 }  // namespace fp8lin
