@@ -25,6 +25,8 @@ __all__ = [
     "fp8_linear_bwd_workspace", "fp8_linear_bwd_workspace_codes", "fp8_linear_fwd_x8_offset",
     "fp8_linear_fwd_w8_offset",
     "GROUP_LINE", "GROUP_TILE", "fp8_quantize_block", "fp8_mm_block", "fp8_mm_block_workspace",
+    "fp8_linear_block_fwd", "fp8_linear_block_bwd", "fp8_linear_block_saved",
+    "fp8_linear_block_fwd_workspace", "fp8_linear_block_bwd_workspace",
     "fp8_moe", "fp8_moe_workspace",
     "EXPORTED_SYMBOLS",
 ]
@@ -45,8 +47,10 @@ EXPORTED_SYMBOLS = (
     "fp8_quantize_colsum_noalloc", "fp8_linear_fwd_workspace",
     "fp8_linear_fwd_x8_offset", "fp8_linear_fwd_w8_offset", "fp8_linear_fwd",
     "fp8_linear_bwd_workspace", "fp8_linear_bwd_workspace_codes", "fp8_linear_bwd",
-    "fp8_quantize_block", "fp8_mm_block_workspace", "fp8_mm_block", "fp8_moe_workspace",
-    "fp8_moe",
+    "fp8_quantize_block", "fp8_mm_block_workspace", "fp8_mm_block",
+    "fp8_linear_block_saved", "fp8_linear_block_fwd_workspace",
+    "fp8_linear_block_bwd_workspace", "fp8_linear_block_fwd", "fp8_linear_block_bwd",
+    "fp8_moe_workspace", "fp8_moe",
     "fp8_last_error", "fp8_version",
 )
 
@@ -110,6 +114,13 @@ def _load() -> ctypes.CDLL:
         "fp8_mm_block_workspace": (S, [I64, I64, I64]),
         "fp8_mm_block": (I32, [P, P, I32, I32, I32, I32, I64, I64, I64, I64, I64, P, I32, P, I32,
                                P, P, P, S, P]),
+        "fp8_linear_block_saved": (S, [I64, I64, I64, I32, I32]),
+        "fp8_linear_block_fwd_workspace": (S, [I64, I64, I64]),
+        "fp8_linear_block_bwd_workspace": (S, [I64, I64, I64]),
+        "fp8_linear_block_fwd": (I32, [P, P, P, P, I32, P, I64, I64, I64, I32, I32, P, S, I32, I32,
+                                       P, S, P, P]),
+        "fp8_linear_block_bwd": (I32, [P, P, S, P, P, I32, I64, I64, I64, I32, I32, I32, I32, I32,
+                                       P, S, P, P, P, P]),
         "fp8_moe_workspace": (S, [I64, I64, I64, I64, I64]),
         "fp8_moe": (I32, [P, P, P, P, P, P, I64, I64, I64, I64, I64, I32, I32, P, S, P, P, P, P]),
         "fp8_last_error": (ctypes.c_char_p, []),
@@ -685,6 +696,79 @@ def fp8_mm_block(a: torch.Tensor, b: torch.Tensor, fmt_a: int, fmt_b: int, trans
                            0 if workspace is None else _ws_bytes(workspace, "workspace"),
                            _stream(stream))
     _check(st, "fp8_mm_block")
+
+
+def fp8_linear_block_saved(M: int, N: int, K: int, want_dx: bool, want_dw: bool) -> int:
+    return int(_lib.fp8_linear_block_saved(M, N, K, int(want_dx), int(want_dw)))
+
+
+def fp8_linear_block_fwd_workspace(M: int, N: int, K: int) -> int:
+    return int(_lib.fp8_linear_block_fwd_workspace(M, N, K))
+
+
+def fp8_linear_block_bwd_workspace(M: int, N: int, K: int) -> int:
+    return int(_lib.fp8_linear_block_bwd_workspace(M, N, K))
+
+
+def _check_block_weight(w8, sw, N: int, K: int) -> None:
+    _buf(w8, "w8", N * K, _BYTE1, nullable=False)
+    _buf(sw, "sw", _groups(N) * _groups(K), _F32, nullable=False)
+
+
+def fp8_linear_block_fwd(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_dw, workspace,
+                         out, w8=None, sw=None, fmt_w=E4M3, stream=None) -> None:
+    """Forward of the linear layer with block scaling; ``saved`` receives
+    what the backward's wanted gradients need; see fp8lin.h."""
+    M, N, K = int(M), int(N), int(K)
+    if min(M, N, K) < 0:
+        raise ValueError("fp8_linear_block_fwd: negative size")
+    _buf(x, "x", M * K, _BF16, nullable=False)
+    _buf(w, "w", N * K, _BF16)
+    if w8 is not None:
+        _check_block_weight(w8, sw, N, K)
+    _buf(bias, "bias", N, _BF16)
+    _buf(out, "out", M * N, _BF16, nullable=False)
+    _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_dw, workspace,
+                           out, w8, sw, fmt_w, stream)
+
+
+def _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_dw, workspace,
+                           out, w8, sw, fmt_w, stream=None) -> None:
+    """fp8_linear_block_fwd's call itself (see _linear_fwd_call)."""
+    st = _lib.fp8_linear_block_fwd(_ptr(x), _ptr(w), _ptr(w8), _ptr(sw), fmt_w, _ptr(bias), M, N,
+                                   K, fmt, margin, _ptr(saved),
+                                   0 if saved is None else _ws_bytes(saved, "saved"),
+                                   int(want_dx), int(want_dw), _ptr(workspace),
+                                   _ws_bytes(workspace, "workspace"), _ptr(out), _stream(stream))
+    _check(st, "fp8_linear_block_fwd")
+
+
+def fp8_linear_block_bwd(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
+                         dw, db, w8=None, sw=None, fmt_w=E4M3, stream=None) -> None:
+    """Gradients of the linear layer with block scaling; see fp8lin.h."""
+    M, N, K = int(M), int(N), int(K)
+    if min(M, N, K) < 0:
+        raise ValueError("fp8_linear_block_bwd: negative size")
+    _buf(g, "g", M * N, _BF16, nullable=False)
+    if w8 is not None:
+        _check_block_weight(w8, sw, N, K)
+    _buf(dx, "dx", M * K, _BF16)
+    _buf(dw, "dw", N * K, _BF16)
+    _buf(db, "db", N, _BF16)
+    _linear_block_bwd_call(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
+                           dw, db, w8, sw, fmt_w, stream)
+
+
+def _linear_block_bwd_call(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
+                           dw, db, w8, sw, fmt_w, stream=None) -> None:
+    """fp8_linear_block_bwd's call itself (see _linear_fwd_call)."""
+    st = _lib.fp8_linear_block_bwd(_ptr(g), _ptr(saved),
+                                   0 if saved is None else _ws_bytes(saved, "saved"), _ptr(w8),
+                                   _ptr(sw), fmt_w, M, N, K, fmt, fmt_g, margin, int(want_dx),
+                                   int(want_dw), _ptr(workspace),
+                                   _ws_bytes(workspace, "workspace"), _ptr(dx), _ptr(dw),
+                                   _ptr(db), _stream(stream))
+    _check(st, "fp8_linear_block_bwd")
 
 
 def fp8_moe_workspace(tokens: int, experts: int, top_k: int, dim: int, hidden: int) -> int:

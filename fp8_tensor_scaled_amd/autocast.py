@@ -21,6 +21,7 @@ Every number is computed in libfp8lin (``fp8_linear_fwd`` /
 ``fp8_linear_bwd`` under dynamic scaling; under delayed scaling the
 forward's quantize and GEMM entry points, which read x and w once per step
 and keep the backward's codes, and ``fp8_linear_bwd`` given those codes;
+``fp8_linear_block_fwd`` / ``fp8_linear_block_bwd`` under block scaling;
 ``fp8_quantize`` / ``fp8_mm`` for pre-quantized weights); this module only
 keeps the rings, picks formats, allocates outputs and reshapes.  Inputs,
 weights and biases are bf16.
@@ -48,12 +49,14 @@ import weakref
 
 import torch
 
-from . import (E4M3, E5M2, GROUP_LINE, GROUP_TILE, OUT_BF16, Ring, _groups, _linear_bwd_call,
-               _linear_fwd_call, _stream, fp8_colsum, fp8_colsum_workspace,
+from . import (E4M3, E5M2, OUT_BF16, Ring, _groups, _linear_block_bwd_call,
+               _linear_block_fwd_call, _linear_bwd_call, _linear_fwd_call, _stream,
+               fp8_colsum, fp8_colsum_workspace,
+               fp8_linear_block_bwd_workspace, fp8_linear_block_fwd_workspace,
+               fp8_linear_block_saved,
                fp8_linear_bwd, fp8_linear_bwd_workspace, fp8_linear_bwd_workspace_codes,
-               fp8_linear_fwd, fp8_linear_fwd_workspace, fp8_mm, fp8_mm_block,
-               fp8_mm_block_workspace, fp8_mm_ex, fp8_quantize, fp8_quantize_block,
-               fp8_quantize_colsum)
+               fp8_linear_fwd, fp8_linear_fwd_workspace, fp8_mm,
+               fp8_mm_ex, fp8_quantize, fp8_quantize_colsum)
 
 __all__ = ["FP8Format", "FP8Recipe", "FP8TensorMeta", "FP8State", "fp8_state", "fp8_autocast",
            "current_config", "fp8_linear", "FP8Linear", "fp8_linear_enable",
@@ -413,17 +416,14 @@ class _LinearFp8Weight(torch.autograd.Function):
 
 
 @functools.lru_cache(maxsize=256)
-def _block_ws_size(m: int, n: int, k: int) -> int:
-    return fp8_mm_block_workspace(m, n, k)
+def _block_ws_sizes(M: int, N: int, K: int) -> tuple:
+    """(forward, backward) workspace bytes of a block-scaled linear call shape."""
+    return (fp8_linear_block_fwd_workspace(M, N, K), fp8_linear_block_bwd_workspace(M, N, K))
 
 
-def _mm_block(a, b, fmt_a, fmt_b, trans_a, trans_b, m, n, k, sa, sb, group_b, bias, out) -> None:
-    """fp8_mm_block on dense operands, with the stream's workspace.  (Its
-    counters lie in the part that the linear calls keep at zero too.)"""
-    need = _block_ws_size(m, n, k)
-    fp8_mm_block(a, b, fmt_a, fmt_b, trans_a, trans_b, m, n, k, m if trans_a else k,
-                 k if trans_b else n, sa, GROUP_LINE, sb, group_b, bias, out,
-                 _workspace(a.device, need) if need else None)
+@functools.lru_cache(maxsize=256)
+def _block_saved_size(M: int, N: int, K: int, want_dx: bool, want_dw: bool) -> int:
+    return fp8_linear_block_saved(M, N, K, want_dx, want_dw)
 
 
 class _LinearFp8Block(torch.autograd.Function):
@@ -446,65 +446,43 @@ class _LinearFp8Block(torch.autograd.Function):
         x2 = x.reshape(-1, K)
         M = x2.shape[0]
         dev = x.device
-        recipe, fmt = cfg.recipe, cfg.fp8_format.fwd()
-        need_x = grad_enabled and ctx.needs_input_grad[0]
-        need_w = grad_enabled and ctx.needs_input_grad[1]
-        ctx.margin, ctx.fmt, ctx.fmt_bwd = recipe.margin, fmt, cfg.fp8_format.bwd()
-        ctx.has_bias, ctx.x_shape, ctx.mnk = bias is not None, x.shape, (M, N, K)
-        u8, f32 = torch.uint8, torch.float32
+        margin, fmt = cfg.recipe.margin, cfg.fp8_format.fwd()
+        codes = w.dtype in _FP8_DTYPES
+        # (a weight that comes as codes is not copied into what is kept)
+        want_dx = grad_enabled and ctx.needs_input_grad[0] and not codes
+        want_dw = grad_enabled and ctx.needs_input_grad[1]
+        ctx.conf = (M, N, K, fmt, cfg.fp8_format.bwd(), margin, want_dx, want_dw,
+                    _FP8_DTYPES[w.dtype] if codes else fmt)
+        ctx.has_bias, ctx.x_shape = bias is not None, x.shape
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        if w.dtype in _FP8_DTYPES:
-            w8, sw, ctx.fmt_w = w, w_scale, _FP8_DTYPES[w.dtype]
-        else:
-            ctx.fmt_w = fmt
-            w8 = torch.empty((N, K), dtype=u8, device=dev)
-            sw = torch.empty((_groups(N), _groups(K)), dtype=f32, device=dev)
-            fp8_quantize_block(w, N, K, fmt, out_tile=w8, scale_tile=sw, margin=recipe.margin)
-        x8c = sxc = None
-        if need_w:
-            x8c = torch.empty((M, K), dtype=u8, device=dev)
-            sxc = torch.empty((_groups(M), K), dtype=f32, device=dev)
+        saved = None
         if M > 0:
-            x8 = torch.empty((M, K), dtype=u8, device=dev)
-            sx = torch.empty((M, _groups(K)), dtype=f32, device=dev)
-            fp8_quantize_block(x2, M, K, fmt, out_row=x8, scale_row=sx, out_col=x8c,
-                               scale_col=sxc, margin=recipe.margin)
-            _mm_block(x8, w8, fmt, ctx.fmt_w, 0, 1, M, N, K, sx, sw, GROUP_TILE, bias, out)
-        ctx.save_for_backward(x8c, sxc, w8 if need_x else None, sw if need_x else None)
+            need = _block_saved_size(M, N, K, want_dx, want_dw)
+            if need:
+                saved = torch.empty(need, dtype=torch.uint8, device=dev)
+            # buffers sized from the operands here, so the unchecked call
+            _linear_block_fwd_call(x2, None if codes else w, bias, M, N, K, fmt, margin, saved,
+                                   want_dx, want_dw, _workspace(dev, _block_ws_sizes(M, N, K)[0]),
+                                   out, w if codes else None, w_scale, ctx.conf[8])
+        ctx.save_for_backward(saved, w if codes else None, w_scale)
         return out.reshape(*x.shape[:-1], N)
 
     @staticmethod
     def backward(ctx, g):
-        M, N, K = ctx.mnk
-        x8c, sxc, w8, sw = ctx.saved_tensors
-        need_x, need_w = ctx.needs_input_grad[:2]
-        need_b = ctx.has_bias and ctx.needs_input_grad[3]
-        dev, u8, f32, b16 = g.device, torch.uint8, torch.float32, torch.bfloat16
+        M, N, K, fmt, fmt_g, margin, want_dx, want_dw, fmt_w = ctx.conf
+        saved, w8, sw = ctx.saved_tensors
+        need_x, need_w, _, need_b = ctx.needs_input_grad[:4]
+        need_b = need_b and ctx.has_bias
+        dev, b16 = g.device, torch.bfloat16
         make = torch.zeros if M == 0 else torch.empty
         dx = make((M, K), dtype=b16, device=dev) if need_x else None
         dw = make((N, K), dtype=b16, device=dev) if need_w else None
         db = make(N, dtype=b16, device=dev) if need_b else None
-        if M > 0:
-            g2 = _bf16(g.reshape(-1, N), "the output gradient")
-            g8 = sg = g8c = sgc = None
-            if need_x:
-                g8 = torch.empty((M, N), dtype=u8, device=dev)
-                sg = torch.empty((M, _groups(N)), dtype=f32, device=dev)
-            if need_w:
-                g8c = torch.empty((M, N), dtype=u8, device=dev)
-                sgc = torch.empty((_groups(M), N), dtype=f32, device=dev)
-            if need_x or need_w:
-                fp8_quantize_block(g2, M, N, ctx.fmt_bwd, out_row=g8, scale_row=sg,
-                                   out_col=g8c, scale_col=sgc, margin=ctx.margin)
-            if need_x:
-                _mm_block(g8, w8, ctx.fmt_bwd, ctx.fmt_w, 0, 0, M, K, N, sg, sw, GROUP_TILE,
-                          None, dx)
-            if need_w:
-                _mm_block(g8c, x8c, ctx.fmt_bwd, ctx.fmt, 1, 0, N, K, M, sgc, sxc, GROUP_LINE,
-                          None, dw)
-            if need_b:
-                ws = torch.empty(fp8_colsum_workspace(M, N), dtype=u8, device=dev)
-                fp8_colsum(g2, M, N, db, ws)
+        if M > 0 and (need_x or need_w or need_b):
+            _linear_block_bwd_call(_bf16(g.reshape(-1, N), "the output gradient"), saved, M, N, K,
+                                   fmt, fmt_g, margin, want_dx, want_dw,
+                                   _workspace(dev, _block_ws_sizes(M, N, K)[1]), dx, dw, db, w8,
+                                   sw, fmt_w)
         return (None if dx is None else dx.reshape(ctx.x_shape), dw, None, db, None, None)
 
 

@@ -54,6 +54,13 @@ struct BlockGemmLaunch {
 };
 size_t block_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_block_gemm(const BlockGemmLaunch& g, hipStream_t stream);
+// A linear backward's dX (NN) and dW (TN) and, with cf.db, the last pass of
+// its bias gradient: one launch where the tiled kernels take both.
+hipError_t launch_block_gemm_pair(const BlockGemmLaunch& dx, const BlockGemmLaunch& dw,
+                                  const ColsumFinalJob& cf, hipStream_t stream);
+// (what that launch is, where it is one)
+hipError_t launch_block_pair(const BlockGemmLaunch& dx, const BlockGemmLaunch& dw,
+                             const ColsumFinalJob& cf, hipStream_t stream);
 
 struct MoeLaunch {
     const uint16_t* x = nullptr;       // bf16 [tokens][dim]

@@ -166,6 +166,259 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
     return e == hipSuccess ? FP8_OK : hip_fail(e, "block gemm launch");
 }
 
+}  // extern "C"
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// What the forward leaves for the backward: x's codes and steps by columns
+// (for dW), w's by tiles (for dX, when they are made here).
+struct SavedLayout {
+    size_t x8, sx, w8, sw, total;
+};
+SavedLayout saved_layout(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw) {
+    SavedLayout l{};
+    size_t at = 0;
+    if (want_dw) {
+        l.x8 = at;
+        at = up256(at + (size_t)M * K);
+        l.sx = at;
+        at = up256(at + 4 * (size_t)groups_of(M) * K);
+    }
+    if (want_dx) {
+        l.w8 = at;
+        at = up256(at + (size_t)N * K);
+        l.sw = at;
+        at = up256(at + 4 * (size_t)groups_of(N) * groups_of(K));
+    }
+    l.total = at;
+    return l;
+}
+
+// Workspaces begin with the per-tensor layer's control block, which these
+// calls leave alone (it stays zero), so that both can share one.
+constexpr size_t kControl = 6656;
+struct FwdWs {
+    size_t x8, sx, w8, sw, total;
+};
+FwdWs fwd_ws(int64_t M, int64_t N, int64_t K) {
+    FwdWs l;
+    l.x8 = kControl;
+    l.sx = up256(l.x8 + (size_t)M * K);
+    l.w8 = up256(l.sx + 4 * (size_t)M * groups_of(K));
+    l.sw = up256(l.w8 + (size_t)N * K);
+    l.total = up256(l.sw + 4 * (size_t)groups_of(N) * groups_of(K));
+    return l;
+}
+struct BwdWs {
+    size_t g8, sg, g8c, sgc, sums, total;
+};
+BwdWs bwd_ws(int64_t M, int64_t N) {
+    BwdWs l;
+    l.g8 = kControl;
+    l.sg = up256(l.g8 + (size_t)M * N);
+    l.g8c = up256(l.sg + 4 * (size_t)M * groups_of(N));
+    l.sgc = up256(l.g8c + (size_t)M * N);
+    l.sums = up256(l.sgc + 4 * (size_t)groups_of(M) * N);
+    const size_t sums = 4 * (size_t)groups_of(M) * N, colsum = fp8lin::colsum_workspace(M, N);
+    l.total = up256(l.sums + (sums > colsum ? sums : colsum));
+    return l;
+}
+
+fp8_status_t check_layer(const char* who, int64_t M, int64_t N, int64_t K, int32_t margin) {
+    if (M < 1 || N < 1 || K < 1)
+        return fail(FP8_EINVAL, "%s: M, N, K must be >= 1 (got %lld, %lld, %lld)", who,
+                    (long long)M, (long long)N, (long long)K);
+    const double lim = 1099511627776.0;
+    if ((double)M * N >= lim || (double)M * K >= lim || (double)N * K >= lim)
+        return fail(FP8_EINVAL, "%s: a matrix is too large", who);
+    const double blocks = 2147483647.0 / 2;
+    if ((double)groups_of(M) * groups_of(N) >= blocks ||
+        (double)groups_of(M) * groups_of(K) >= blocks ||
+        (double)groups_of(N) * groups_of(K) >= blocks)
+        return fail(FP8_EINVAL, "%s: too many blocks", who);
+    if (margin < 0 || margin > 64)
+        return fail(FP8_EINVAL, "%s: margin %d outside [0, 64]", who, margin);
+    return FP8_OK;
+}
+
+fp8_status_t check_scratch(const char* who, const char* what, const void* p, size_t have,
+                           size_t need) {
+    if (need == 0) return FP8_OK;
+    if (!p) return fail(FP8_EINVAL, "%s: %s is NULL", who, what);
+    if (have < need) return fail(FP8_EINVAL, "%s: %s %zu < %zu bytes", who, what, have, need);
+    if ((uintptr_t)p & 255) return fail(FP8_EINVAL, "%s: %s not 256-byte aligned", who, what);
+    return FP8_OK;
+}
+
+fp8lin::BlockQuantLaunch quant_of(const uint16_t* x, int64_t rows, int64_t cols, fp8_fmt_t fmt,
+                                  int32_t margin) {
+    fp8lin::BlockQuantLaunch q;
+    q.x = x;
+    q.in_type = FP8_IN_BF16;
+    q.rows = rows;
+    q.cols = cols;
+    q.ldx = cols;
+    q.fmt = fmt;
+    q.rmargin = ldexpf(1.0f, -margin);
+    return q;
+}
+
+fp8lin::BlockGemmLaunch gemm_of(const uint8_t* a, const uint8_t* b, fp8_fmt_t fa, fp8_fmt_t fb,
+                                int ta, int tb, int64_t m, int64_t n, int64_t k, const float* sa,
+                                const float* sb, fp8_group_t group_b, const uint16_t* bias,
+                                uint16_t* out) {
+    fp8lin::BlockGemmLaunch g;
+    g.a = a;
+    g.b = b;
+    g.fmt_a = fa;
+    g.fmt_b = fb;
+    g.trans_a = ta;
+    g.trans_b = tb;
+    g.m = m;
+    g.n = n;
+    g.k = k;
+    g.lda = ta ? m : k;
+    g.ldb = tb ? k : n;
+    g.sa = scale_of(sa, FP8_GROUP_LINE, ta == 0, m, k);
+    g.sb = scale_of(sb, group_b, tb != 0, n, k);
+    g.bias = bias;
+    g.out = out;
+    return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp8_linear_block_saved(int64_t M, int64_t N, int64_t K, int32_t want_dx, int32_t want_dw) {
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return saved_layout(M, N, K, want_dx != 0, want_dw != 0).total;
+}
+size_t fp8_linear_block_fwd_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return fwd_ws(M, N, K).total;
+}
+size_t fp8_linear_block_bwd_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return bwd_ws(M, N).total;
+}
+
+fp8_status_t fp8_linear_block_fwd(const uint16_t* x, const uint16_t* w, const uint8_t* w8,
+                                  const float* sw, fp8_fmt_t fmt_w, const uint16_t* bias,
+                                  int64_t M, int64_t N, int64_t K, fp8_fmt_t fmt, int32_t margin,
+                                  void* saved, size_t saved_bytes, int32_t want_dx,
+                                  int32_t want_dw, void* workspace, size_t workspace_bytes,
+                                  uint16_t* out, hipStream_t stream) {
+    clear_error();
+    const char* who = "fp8_linear_block_fwd";
+    if (!fmt_ok(fmt) || (w8 && !fmt_ok(fmt_w)))
+        return fail(FP8_EINVAL, "%s: unsupported fp8 format", who);
+    if (!x || !out) return fail(FP8_EINVAL, "%s: x or out is NULL", who);
+    if ((w != nullptr) == (w8 != nullptr))
+        return fail(FP8_EINVAL, "%s: the weight comes either as bf16 or as codes", who);
+    if (w8 && !sw) return fail(FP8_EINVAL, "%s: codes of the weight need their steps", who);
+    fp8_status_t st = check_layer(who, M, N, K, margin);
+    if (st) return st;
+    // a weight given as codes is its caller's to keep
+    const SavedLayout S = saved_layout(M, N, K, want_dx && w, want_dw != 0);
+    if ((st = check_scratch(who, "saved", saved, saved_bytes, S.total))) return st;
+    const FwdWs L = fwd_ws(M, N, K);
+    if ((st = check_scratch(who, "workspace", workspace, workspace_bytes, L.total))) return st;
+    if ((st = check_device())) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* sv = static_cast<uint8_t*>(saved);
+    fp8lin::BlockQuantLaunch qx = quant_of(x, M, K, fmt, margin);
+    qx.out_row = ws + L.x8;
+    qx.scale_row = reinterpret_cast<float*>(ws + L.sx);
+    if (want_dw) {
+        qx.out_col = sv + S.x8;
+        qx.scale_col = reinterpret_cast<float*>(sv + S.sx);
+    }
+    hipError_t e;
+    if (w) {
+        uint8_t* at = want_dx ? sv + S.w8 : ws + L.w8;
+        float* steps = reinterpret_cast<float*>(want_dx ? sv + S.sw : ws + L.sw);
+        fp8lin::BlockQuantLaunch qw = quant_of(w, N, K, fmt, margin);
+        qw.out_tile = at;
+        qw.scale_tile = steps;
+        e = fp8lin::launch_quantize_block_two(qx, qw, stream);
+        w8 = at;
+        sw = steps;
+        fmt_w = fmt;
+    } else {
+        e = fp8lin::launch_quantize_block(qx, stream);
+    }
+    if (e != hipSuccess) return hip_fail(e, "block quantize launch");
+    e = fp8lin::launch_block_gemm(gemm_of(qx.out_row, w8, fmt, fmt_w, 0, 1, M, N, K, qx.scale_row,
+                                          sw, FP8_GROUP_TILE, bias, out), stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "block gemm launch");
+}
+
+fp8_status_t fp8_linear_block_bwd(const uint16_t* g, const void* saved, size_t saved_bytes,
+                                  const uint8_t* w8, const float* sw, fp8_fmt_t fmt_w, int64_t M,
+                                  int64_t N, int64_t K, fp8_fmt_t fmt, fp8_fmt_t fmt_g,
+                                  int32_t margin, int32_t want_dx, int32_t want_dw,
+                                  void* workspace, size_t workspace_bytes, uint16_t* dx,
+                                  uint16_t* dw, uint16_t* db, hipStream_t stream) {
+    clear_error();
+    const char* who = "fp8_linear_block_bwd";
+    if (!fmt_ok(fmt) || !fmt_ok(fmt_g) || (w8 && !fmt_ok(fmt_w)))
+        return fail(FP8_EINVAL, "%s: unsupported fp8 format", who);
+    if (!g) return fail(FP8_EINVAL, "%s: g is NULL", who);
+    if (w8 && !sw) return fail(FP8_EINVAL, "%s: codes of the weight need their steps", who);
+    fp8_status_t st = check_layer(who, M, N, K, margin);
+    if (st) return st;
+    if ((dx && !w8 && !want_dx) || (dw && !want_dw))
+        return fail(FP8_EINVAL, "%s: a gradient whose codes the forward did not keep", who);
+    const SavedLayout S = saved_layout(M, N, K, want_dx && !w8, want_dw != 0);
+    if ((st = check_scratch(who, "saved", saved, saved_bytes, S.total))) return st;
+    const BwdWs L = bwd_ws(M, N);
+    if ((st = check_scratch(who, "workspace", workspace, workspace_bytes, L.total))) return st;
+    if ((st = check_device())) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const uint8_t* sv = static_cast<const uint8_t*>(saved);
+    hipError_t e = hipSuccess;
+    fp8lin::ColsumFinalJob cf;
+    fp8lin::BlockQuantLaunch q = quant_of(g, M, N, fmt_g, margin);
+    if (dx) {
+        q.out_row = ws + L.g8;
+        q.scale_row = reinterpret_cast<float*>(ws + L.sg);
+    }
+    if (dw) {
+        q.out_col = ws + L.g8c;
+        q.scale_col = reinterpret_cast<float*>(ws + L.sgc);
+    }
+    if (db && dx && dw) {  // its partial sums come from the quantize's read of g
+        q.sums = reinterpret_cast<float*>(ws + L.sums);
+        cf.part = q.sums;
+        cf.chunks = groups_of(M);
+        cf.n = N;
+        cf.db = db;
+    } else if (db) {
+        e = fp8lin::launch_colsum(g, M, N, db, ws + L.sums, stream);
+        if (e != hipSuccess) return hip_fail(e, "colsum launch");
+    }
+    if (!dx && !dw) return FP8_OK;
+    e = fp8lin::launch_quantize_block(q, stream);
+    if (e != hipSuccess) return hip_fail(e, "block quantize launch");
+    if (!w8) {
+        w8 = sv + S.w8;
+        sw = reinterpret_cast<const float*>(sv + S.sw);
+        fmt_w = fmt;
+    }
+    // dX[M][K] = g8[M][N] . w8[N][K] (NN); dW[N][K] = g8c^T . x8c (TN)
+    const fp8lin::BlockGemmLaunch gx = gemm_of(q.out_row, w8, fmt_g, fmt_w, 0, 0, M, K, N,
+                                               q.scale_row, sw, FP8_GROUP_TILE, nullptr, dx);
+    const fp8lin::BlockGemmLaunch gw =
+        gemm_of(q.out_col, sv + S.x8, fmt_g, fmt, 1, 0, N, K, M, q.scale_col,
+                reinterpret_cast<const float*>(sv + S.sx), FP8_GROUP_LINE, nullptr, dw);
+    if (dx && dw) e = fp8lin::launch_block_gemm_pair(gx, gw, cf, stream);
+    else e = fp8lin::launch_block_gemm(dx ? gx : gw, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "block gemm launch");
+}
+
 static const char* moe_sizes_error(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim,
                                    int64_t hidden) {
     if (tokens < 0 || tokens > 1024) return "tokens outside [0, 1024]";

@@ -236,6 +236,10 @@ static bool tiled_supported(const BlockGemmLaunch& g) {
     return (double)((g.m + 127) / 128) * (double)((g.n + 127) / 128) < lim;
 }
 
+// A backward's products go in one launch of 128 x 128 tiles up to this many of
+// them (four rounds of the CUs); beyond, each gains more from larger tiles.
+constexpr int kPairTiles = 1024;
+
 static BlockCfg tile_cfg(const BlockGemmLaunch& g) {
     auto rounds = [&](int bm, int bn) {
         return (((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn) + 255) / 256;
@@ -243,6 +247,21 @@ static BlockCfg tile_cfg(const BlockGemmLaunch& g) {
     const BlockCfg half = g.n >= g.m ? BlockCfg::kWide : BlockCfg::kTall;
     const int64_t half_rounds = g.n >= g.m ? rounds(128, 256) : rounds(256, 128);
     return half_rounds * 675 <= rounds(128, 128) * 475 ? half : BlockCfg::kMid;
+}
+
+hipError_t launch_block_gemm_pair(const BlockGemmLaunch& dx, const BlockGemmLaunch& dw,
+                                  const ColsumFinalJob& cf, hipStream_t stream) {
+    auto tiles = [](const BlockGemmLaunch& g) {
+        return (double)((g.m + 127) / 128) * (double)((g.n + 127) / 128);
+    };
+    if (tiled_supported(dx) && tiled_supported(dw) && dx.fmt_b == dw.fmt_b &&
+        dx.fmt_a == dw.fmt_a && dx.sb.shift != 0 && dw.sb.shift == 0 &&
+        tiles(dx) + tiles(dw) <= kPairTiles)
+        return launch_block_pair(dx, dw, cf, stream);
+    hipError_t e = launch_block_gemm(dx, stream);
+    if (e == hipSuccess) e = launch_block_gemm(dw, stream);
+    if (e == hipSuccess && cf.db) e = launch_colsum_final_job(cf, stream);
+    return e;
 }
 
 hipError_t launch_block_gemm(const BlockGemmLaunch& g, hipStream_t stream) {

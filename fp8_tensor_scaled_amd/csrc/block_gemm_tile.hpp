@@ -68,10 +68,11 @@ struct BlockTile {
     static_assert(kLds <= 160 * 1024, "LDS");
 };
 
+// One output tile: workgroup `bid` of a grid of `wgs` over problem p.
 template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
-__global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTileParams p) {
+__device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bid, int wgs,
+                                                uint8_t* smem) {
     using BT = BlockTile<BVEC, BM, BN, WM, WN, ST>;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[BT::kLds];
     constexpr int NW = BT::NW, BK = kGroup, kStage = BT::kStage, kPer = BT::kPer;
     constexpr int kStageA = BM * BK;
     constexpr int TM = BM / WM, TN = BN / WN;
@@ -89,8 +90,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTilePar
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
 
-    int bid = blockIdx.x;
-    if (p.xcd_remap) bid = (bid & 7) * ((int)gridDim.x >> 3) + (bid >> 3);
+    if (p.xcd_remap) bid = (bid & 7) * (wgs >> 3) + (bid >> 3);
     const int per_group = p.group_m * p.tiles_n;
     const int first_m = (bid / per_group) * p.group_m;
     const int gsz = p.tiles_m - first_m < p.group_m ? p.tiles_m - first_m : p.group_m;
@@ -355,13 +355,20 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTilePar
     }
 }
 
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTileParams p) {
+    __shared__ __attribute__((aligned(1024)))
+    uint8_t smem[BlockTile<BVEC, BM, BN, WM, WN, ST>::kLds];
+    block_gemm_tile<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST>(p, blockIdx.x, gridDim.x, smem);
+}
+
 enum class BlockCfg { kWide, kTall, kMid };
 hipError_t launch_block_nt(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
 hipError_t launch_block_nn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
 hipError_t launch_block_tn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
 
-template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
-hipError_t launch_block_tile(const BlockGemmLaunch& g, hipStream_t stream) {
+template <int BM, int BN>
+BlockTileParams block_tile_params(const BlockGemmLaunch& g) {
     BlockTileParams p{};
     p.a = g.a;
     p.b = g.b;
@@ -380,10 +387,15 @@ hipError_t launch_block_tile(const BlockGemmLaunch& g, hipStream_t stream) {
     const uintptr_t ob = reinterpret_cast<uintptr_t>(g.out);
     const uintptr_t bb = reinterpret_cast<uintptr_t>(g.bias);
     p.vec_out16 = (ob & 15) == 0 && g.n % 8 == 0 && (bb & 7) == 0;
-    const int total = p.tiles_m * p.tiles_n;
-    p.xcd_remap = total % 8 == 0;
+    p.xcd_remap = p.tiles_m * p.tiles_n % 8 == 0;
+    return p;
+}
+
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+hipError_t launch_block_tile(const BlockGemmLaunch& g, hipStream_t stream) {
+    const BlockTileParams p = block_tile_params<BM, BN>(g);
     hipLaunchKernelGGL((block_gemm_kernel<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST>),
-                       dim3((unsigned)total), dim3(WM * WN * 64), 0, stream, p);
+                       dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(WM * WN * 64), 0, stream, p);
     return hipGetLastError();
 }
 

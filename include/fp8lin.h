@@ -525,6 +525,46 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
                           hipStream_t stream);
 
 /* ---------------------------------------------------------------------
+ * fp8_linear_block_fwd / _bwd -- the linear layer with block scaling.
+ *
+ *   out[M][N] = x8 . w8^T + bias      x by rows (groups along K), w by tiles
+ *   dx[M][K]  = g8 . w8               g by rows (groups along N), w as in the forward
+ *   dw[N][K]  = g8'^T . x8'           g and x by columns (groups along M)
+ *   db[N]     = bf16( sum_m g[m][:] )
+ *
+ * in the arithmetic of fp8_quantize_block and fp8_mm_block; x and w are
+ * quantized in fmt, g in fmt_g.  Two launches forward and two backward when
+ * all three gradients are asked (more for sizes or formats that the tiled
+ * products do not take).
+ * w: bf16 [N][K]; or NULL with w8, sw: its codes in fmt_w and the steps of
+ *     their tiles, used as they are.
+ * saved: device buffer of fp8_linear_block_saved(M, N, K, want_dx, want_dw)
+ *     bytes (0: may be NULL), 256-byte aligned: what the forward keeps for the gradients
+ *     that a backward will ask; the same flags go to both calls.  A weight
+ *     given as codes is not kept: give want_dx 0 to the size, and w8, sw to
+ *     the backward.
+ * workspace: fp8_linear_block_fwd_workspace / _bwd_workspace(M, N, K) bytes,
+ *     256-byte aligned; its first 6656 bytes are left as they are, so that
+ *     it can be the per-tensor layer's too.
+ * dx, dw, db: each NULL to skip that gradient.  bias: bf16 [N] or NULL.
+ * ------------------------------------------------------------------- */
+size_t fp8_linear_block_saved(int64_t M, int64_t N, int64_t K, int32_t want_dx, int32_t want_dw);
+size_t fp8_linear_block_fwd_workspace(int64_t M, int64_t N, int64_t K);
+size_t fp8_linear_block_bwd_workspace(int64_t M, int64_t N, int64_t K);
+fp8_status_t fp8_linear_block_fwd(const uint16_t* x, const uint16_t* w, const uint8_t* w8,
+                                  const float* sw, fp8_fmt_t fmt_w, const uint16_t* bias,
+                                  int64_t M, int64_t N, int64_t K, fp8_fmt_t fmt, int32_t margin,
+                                  void* saved, size_t saved_bytes, int32_t want_dx,
+                                  int32_t want_dw, void* workspace, size_t workspace_bytes,
+                                  uint16_t* out, hipStream_t stream);
+fp8_status_t fp8_linear_block_bwd(const uint16_t* g, const void* saved, size_t saved_bytes,
+                                  const uint8_t* w8, const float* sw, fp8_fmt_t fmt_w, int64_t M,
+                                  int64_t N, int64_t K, fp8_fmt_t fmt, fp8_fmt_t fmt_g,
+                                  int32_t margin, int32_t want_dx, int32_t want_dw,
+                                  void* workspace, size_t workspace_bytes, uint16_t* dx,
+                                  uint16_t* dw, uint16_t* db, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
  * fp8_moe -- a whole mixture-of-experts layer for a few tokens.
  *
  *   l = x R^T (fp32);  e_1 .. e_k = the top_k largest of l, ties to the
