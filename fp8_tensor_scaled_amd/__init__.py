@@ -728,19 +728,28 @@ def fp8_linear_block_fwd(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_
         _check_block_weight(w8, sw, N, K)
     _buf(bias, "bias", N, _BF16)
     _buf(out, "out", M * N, _BF16, nullable=False)
-    _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_dw, workspace,
-                           out, w8, sw, fmt_w, stream)
+    for t in (x, w, bias, out, w8, sw):
+        _ptr(t)
+    _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved,
+                           0 if saved is None else _ws_bytes(saved, "saved"), want_dx, want_dw,
+                           workspace, _ws_bytes(workspace, "workspace"), out, w8, sw, fmt_w,
+                           _stream(stream))
 
 
-def _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved, want_dx, want_dw, workspace,
-                           out, w8, sw, fmt_w, stream=None) -> None:
-    """fp8_linear_block_fwd's call itself (see _linear_fwd_call)."""
-    st = _lib.fp8_linear_block_fwd(_ptr(x), _ptr(w), _ptr(w8), _ptr(sw), fmt_w, _ptr(bias), M, N,
-                                   K, fmt, margin, _ptr(saved),
-                                   0 if saved is None else _ws_bytes(saved, "saved"),
-                                   int(want_dx), int(want_dw), _ptr(workspace),
-                                   _ws_bytes(workspace, "workspace"), _ptr(out), _stream(stream))
-    _check(st, "fp8_linear_block_fwd")
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _linear_block_fwd_call(x, w, bias, M, N, K, fmt, margin, saved, saved_bytes, want_dx, want_dw,
+                           workspace, workspace_bytes, out, w8, sw, fmt_w, stream) -> None:
+    """fp8_linear_block_fwd's call itself, for callers whose buffers are on
+    the GPU and sized for (M, N, K) by construction."""
+    st = _lib.fp8_linear_block_fwd(x.data_ptr(), _addr(w), _addr(w8), _addr(sw), fmt_w,
+                                   _addr(bias), M, N, K, fmt, margin, _addr(saved), saved_bytes,
+                                   want_dx, want_dw, workspace.data_ptr(), workspace_bytes,
+                                   out.data_ptr(), stream)
+    if st:
+        _check(st, "fp8_linear_block_fwd")
 
 
 def fp8_linear_block_bwd(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
@@ -755,20 +764,23 @@ def fp8_linear_block_bwd(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw
     _buf(dx, "dx", M * K, _BF16)
     _buf(dw, "dw", N * K, _BF16)
     _buf(db, "db", N, _BF16)
-    _linear_block_bwd_call(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
-                           dw, db, w8, sw, fmt_w, stream)
+    for t in (g, dx, dw, db, w8, sw):
+        _ptr(t)
+    _linear_block_bwd_call(g, saved, 0 if saved is None else _ws_bytes(saved, "saved"), M, N, K,
+                           fmt, fmt_g, margin, want_dx, want_dw, workspace,
+                           _ws_bytes(workspace, "workspace"), dx, dw, db, w8, sw, fmt_w,
+                           _stream(stream))
 
 
-def _linear_block_bwd_call(g, saved, M, N, K, fmt, fmt_g, margin, want_dx, want_dw, workspace, dx,
-                           dw, db, w8, sw, fmt_w, stream=None) -> None:
-    """fp8_linear_block_bwd's call itself (see _linear_fwd_call)."""
-    st = _lib.fp8_linear_block_bwd(_ptr(g), _ptr(saved),
-                                   0 if saved is None else _ws_bytes(saved, "saved"), _ptr(w8),
-                                   _ptr(sw), fmt_w, M, N, K, fmt, fmt_g, margin, int(want_dx),
-                                   int(want_dw), _ptr(workspace),
-                                   _ws_bytes(workspace, "workspace"), _ptr(dx), _ptr(dw),
-                                   _ptr(db), _stream(stream))
-    _check(st, "fp8_linear_block_bwd")
+def _linear_block_bwd_call(g, saved, saved_bytes, M, N, K, fmt, fmt_g, margin, want_dx, want_dw,
+                           workspace, workspace_bytes, dx, dw, db, w8, sw, fmt_w, stream) -> None:
+    """fp8_linear_block_bwd's call itself (see _linear_block_fwd_call)."""
+    st = _lib.fp8_linear_block_bwd(g.data_ptr(), _addr(saved), saved_bytes, _addr(w8), _addr(sw),
+                                   fmt_w, M, N, K, fmt, fmt_g, margin, want_dx, want_dw,
+                                   workspace.data_ptr(), workspace_bytes, _addr(dx), _addr(dw),
+                                   _addr(db), stream)
+    if st:
+        _check(st, "fp8_linear_block_bwd")
 
 
 def fp8_moe_workspace(tokens: int, experts: int, top_k: int, dim: int, hidden: int) -> int:

@@ -426,6 +426,15 @@ def _block_saved_size(M: int, N: int, K: int, want_dx: bool, want_dw: bool) -> i
     return fp8_linear_block_saved(M, N, K, want_dx, want_dw)
 
 
+def _on_gpu(x, w, bias) -> None:
+    """All operands on one GPU (the calls below hand over plain addresses)."""
+    dev = x.device
+    if dev.type != "cuda" or w.device != dev or (bias is not None and bias.device != dev):
+        raise ValueError(f"fp8_linear: input on {dev}, weight on {w.device}"
+                         + ("" if bias is None else f", bias on {bias.device}")
+                         + ": all must be on one GPU")
+
+
 class _LinearFp8Block(torch.autograd.Function):
     """y = x w^T + b and its gradients with block scaling: x and g have a
     step for each row and group of 128 along the dimension that the product
@@ -461,11 +470,12 @@ class _LinearFp8Block(torch.autograd.Function):
             if need:
                 saved = torch.empty(need, dtype=torch.uint8, device=dev)
             # buffers sized from the operands here, so the unchecked call
+            ws = _workspace(dev, _block_ws_sizes(M, N, K)[0])
             _linear_block_fwd_call(x2, None if codes else w, bias, M, N, K, fmt, margin, saved,
-                                   want_dx, want_dw, _workspace(dev, _block_ws_sizes(M, N, K)[0]),
-                                   out, w if codes else None, w_scale, ctx.conf[8])
+                                   need, want_dx, want_dw, ws, ws.numel(), out,
+                                   w if codes else None, w_scale, ctx.conf[8], _stream())
         ctx.save_for_backward(saved, w if codes else None, w_scale)
-        return out.reshape(*x.shape[:-1], N)
+        return out if x.dim() == 2 else out.reshape(*x.shape[:-1], N)
 
     @staticmethod
     def backward(ctx, g):
@@ -479,11 +489,14 @@ class _LinearFp8Block(torch.autograd.Function):
         dw = make((N, K), dtype=b16, device=dev) if need_w else None
         db = make(N, dtype=b16, device=dev) if need_b else None
         if M > 0 and (need_x or need_w or need_b):
-            _linear_block_bwd_call(_bf16(g.reshape(-1, N), "the output gradient"), saved, M, N, K,
-                                   fmt, fmt_g, margin, want_dx, want_dw,
-                                   _workspace(dev, _block_ws_sizes(M, N, K)[1]), dx, dw, db, w8,
-                                   sw, fmt_w)
-        return (None if dx is None else dx.reshape(ctx.x_shape), dw, None, db, None, None)
+            g2 = _bf16(g.reshape(-1, N), "the output gradient")
+            ws = _workspace(dev, _block_ws_sizes(M, N, K)[1])
+            _linear_block_bwd_call(g2, saved, 0 if saved is None else saved.numel(), M, N, K, fmt,
+                                   fmt_g, margin, want_dx, want_dw, ws, ws.numel(), dx, dw, db,
+                                   w8, sw, fmt_w, _stream())
+        if dx is not None and len(ctx.x_shape) != 2:
+            dx = dx.reshape(ctx.x_shape)
+        return dx, dw, None, db, None, None
 
 
 def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
@@ -518,6 +531,9 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
             if tuple(w_scale.shape) != tiles:
                 raise ValueError(f"fp8_linear: w_scale of shape {tuple(w_scale.shape)}, expected "
                                  f"{tiles} (a step for each 128 x 128 tile)")
+            if w_scale.dtype != torch.float32 or w_scale.device != w.device:
+                raise ValueError("fp8_linear: w_scale must be float32, on the weight's device")
+            _on_gpu(x, w, bias)
             return _LinearFp8Block.apply(_bf16(x, "x"), w.contiguous(), w_scale.contiguous(),
                                          _bf16(bias, "bias"), cfg, torch.is_grad_enabled())
         return _LinearFp8Weight.apply(_bf16(x, "x"), w, w_scale,
@@ -525,6 +541,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = Non
     if not cfg.enabled:
         return torch.nn.functional.linear(x, w, bias)
     if cfg.recipe.block:
+        _on_gpu(x, w, bias)
         return _LinearFp8Block.apply(_bf16(x, "x"), _bf16(w, "w"), None, _bf16(bias, "bias"), cfg,
                                      torch.is_grad_enabled())
     return _LinearFp8.apply(_bf16(x, "x"), _bf16(w, "w"), _bf16(bias, "bias"), cfg,

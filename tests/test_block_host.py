@@ -102,6 +102,93 @@ def test_mm_block_workspace_sizes():
             assert f._lib.fp8_mm_block(*args) == 1 and "workspace" in err()
 
 
+def fwd_args(**over):
+    need = f.fp8_linear_block_saved(4, 200, 300, True, True)
+    a = dict(x=FAKE, w=FAKE, w8=None, sw=None, fmt_w=0, bias=None, M=4, N=200, K=300, fmt=0,
+             margin=0, saved=FAKE, saved_bytes=need, want_dx=1, want_dw=1, workspace=FAKE,
+             workspace_bytes=f.fp8_linear_block_fwd_workspace(4, 200, 300), out=FAKE, stream=None)
+    a.update(over)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("over,needle", [
+    (dict(fmt=2), "format"),
+    (dict(w=None, w8=FAKE, sw=FAKE, fmt_w=5), "format"),
+    (dict(x=None), "NULL"),
+    (dict(out=None), "NULL"),
+    (dict(w=None), "either as bf16 or as codes"),
+    (dict(w8=FAKE, sw=FAKE), "either as bf16 or as codes"),
+    (dict(w=None, w8=FAKE), "need their steps"),
+    (dict(M=0), ">= 1"),
+    (dict(M=1 << 30, K=1 << 20), "too large"),
+    (dict(margin=65), "margin"),
+    (dict(saved=None), "saved is NULL"),
+    (dict(saved_bytes=100), "saved 100 <"),
+    (dict(saved=P(0x1010)), "256-byte"),
+    (dict(workspace=None), "workspace is NULL"),
+    (dict(workspace_bytes=6656), "workspace 6656 <"),
+    (dict(workspace=P(0x1010)), "256-byte"),
+])
+def test_linear_block_fwd_refusals(over, needle):
+    assert f._lib.fp8_linear_block_fwd(*fwd_args(**over)) == 1 and needle in err(), err()
+
+
+def bwd_args(**over):
+    need = f.fp8_linear_block_saved(4, 200, 300, True, True)
+    a = dict(g=FAKE, saved=FAKE, saved_bytes=need, w8=None, sw=None, fmt_w=0, M=4, N=200, K=300,
+             fmt=0, fmt_g=1, margin=0, want_dx=1, want_dw=1, workspace=FAKE,
+             workspace_bytes=f.fp8_linear_block_bwd_workspace(4, 200, 300), dx=FAKE, dw=FAKE,
+             db=None, stream=None)
+    a.update(over)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("over,needle", [
+    (dict(fmt=2), "format"),
+    (dict(fmt_g=2), "format"),
+    (dict(g=None), "g is NULL"),
+    (dict(w8=FAKE), "need their steps"),
+    (dict(K=0), ">= 1"),
+    (dict(margin=-1), "margin"),
+    (dict(want_dx=0), "did not keep"),
+    (dict(want_dw=0), "did not keep"),
+    (dict(saved=None), "saved is NULL"),
+    (dict(saved_bytes=100), "saved 100 <"),
+    (dict(workspace_bytes=7000), "workspace 7000 <"),
+])
+def test_linear_block_bwd_refusals(over, needle):
+    assert f._lib.fp8_linear_block_bwd(*bwd_args(**over)) == 1 and needle in err(), err()
+
+
+def test_linear_block_buffers():
+    """The binding's own checks: sizes, types, and that tensors are on a GPU."""
+    fwd = dict(x=b16(1200), w=b16(60000), bias=None, M=4, N=200, K=300, fmt=0, margin=0,
+               saved=None, want_dx=False, want_dw=False, workspace=u8(1 << 20), out=b16(800))
+    raises("x: 1199 elements", lambda: f.fp8_linear_block_fwd(**dict(fwd, x=b16(1199))))
+    raises("w: 59999 elements", lambda: f.fp8_linear_block_fwd(**dict(fwd, w=b16(59999))))
+    raises("out: 799 elements", lambda: f.fp8_linear_block_fwd(**dict(fwd, out=b16(799))))
+    raises("bias: 199 elements", lambda: f.fp8_linear_block_fwd(**dict(fwd, bias=b16(199))))
+    raises("sw: 5 elements", lambda: f.fp8_linear_block_fwd(**dict(fwd, w=None, w8=u8(60000),
+                                                                   sw=f32(5))))
+    raises("is on cpu, not a GPU", lambda: f.fp8_linear_block_fwd(**fwd))
+    raises("negative size", lambda: f.fp8_linear_block_fwd(**dict(fwd, M=-1)))
+    bwd = dict(g=b16(800), saved=None, M=4, N=200, K=300, fmt=0, fmt_g=1, margin=0, want_dx=False,
+               want_dw=False, workspace=u8(1 << 20), dx=b16(1200), dw=b16(60000), db=b16(200))
+    for name, n in (("g", 800), ("dx", 1200), ("dw", 60000), ("db", 200)):
+        raises(f"{name}: {n - 1} elements",
+               lambda: f.fp8_linear_block_bwd(**dict(bwd, **{name: b16(n - 1)})))
+    raises("is on cpu, not a GPU", lambda: f.fp8_linear_block_bwd(**bwd))
+
+
+def test_linear_block_sizes():
+    assert f.fp8_linear_block_saved(0, 1, 1, True, True) == 0
+    assert f.fp8_linear_block_saved(4, 200, 300, False, False) == 0
+    both = f.fp8_linear_block_saved(4, 200, 300, True, True)
+    assert both >= 4 * 300 + 4 * 300 + 200 * 300 + 4 * 2 * 3
+    assert f.fp8_linear_block_saved(4, 200, 300, True, False) < both
+    assert f.fp8_linear_block_fwd_workspace(4, 200, 300) > 6656 + 4 * 300 + 200 * 300
+
+
 def moe_args(**over):
     a = dict(x=FAKE, router=FAKE, w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, tokens=4, experts=8,
              top_k=2, dim=256, hidden=128, fmt=0, renormalize=1, workspace=FAKE,
@@ -242,6 +329,12 @@ def test_block_recipe():
         x = torch.zeros(2, 300, dtype=torch.bfloat16)
         with pytest.raises(ValueError, match="a step for each 128 x 128 tile"):
             ac.fp8_linear(x, w8, w_scale=torch.ones(1))
+        with pytest.raises(ValueError, match="must be float32"):
+            ac.fp8_linear(x, w8, w_scale=torch.ones(2, 3, dtype=torch.float64))
+        with pytest.raises(ValueError, match="on one GPU"):
+            ac.fp8_linear(x, w8, w_scale=torch.ones(2, 3))
+        with pytest.raises(ValueError, match="on one GPU"):
+            ac.fp8_linear(x, torch.zeros(256, 300, dtype=torch.bfloat16))
         with pytest.raises(ValueError, match="bf16 bias"):
             ac.fp8_linear(x, w8, w_scale=torch.ones(2, 3), b_scale=torch.ones(1),
                           bias=torch.zeros(256, dtype=torch.uint8).view(torch.float8_e4m3fn))
