@@ -607,6 +607,25 @@ def _groups(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
+def _addresses(*specs) -> list:
+    """Device addresses of the tensors of (tensor, name, elements, dtypes):
+    the checks of _buf and _ptr in one step, and those themselves, sizes
+    before devices, where one fails.  Tensors given as None stay None."""
+    got = []
+    for t, _, numel, dtypes in specs:
+        if t is None:
+            got.append(None)
+        elif (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes
+              and t.numel() >= numel and t.is_contiguous()):
+            got.append(t.data_ptr())
+        else:
+            for s in specs:
+                _buf(*s)
+            for s in specs:
+                _ptr(s[0])
+    return got
+
+
 def fp8_quantize_block(x: torch.Tensor, rows: int, cols: int, fmt: int,
                        out_row: torch.Tensor | None = None,
                        scale_row: torch.Tensor | None = None,
@@ -629,40 +648,36 @@ def fp8_quantize_block(x: torch.Tensor, rows: int, cols: int, fmt: int,
             raise ValueError(f"fp8_quantize_block: no input type for dtype {x.dtype}")
     elif in_type not in (IN_BF16, IN_F16, IN_F32):
         raise ValueError(f"fp8_quantize_block: bad input type {in_type}")
-    rows, cols = int(rows), int(cols)
+    elif x.dtype not in (_F32 if in_type == IN_F32 else _BYTE2):
+        raise ValueError(f"x: dtype {x.dtype} for input type {in_type}")
     if ldx is None:
         ldx = cols
     if rows < 0 or cols < 0 or ldx < cols:
         raise ValueError(f"fp8_quantize_block: bad sizes {rows} x {cols}, ldx {ldx}")
-    if x.dtype not in (_F32 if in_type == IN_F32 else _BYTE2):
-        raise ValueError(f"x: dtype {x.dtype} for input type {in_type}")
-    if not x.is_contiguous() and not (x.dim() == 2 and x.stride(1) == 1 and x.stride(0) == ldx):
+    if x.is_contiguous():
+        span = x.numel()
+    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) == ldx:
+        span = (x.shape[0] - 1) * ldx + x.shape[1]
+    else:
         raise ValueError("x: must be contiguous, or 2-D with unit column stride and row stride "
                          "ldx")
     n = rows * cols
-    if n and _span(x) < (rows - 1) * ldx + cols:
-        raise ValueError(f"x: {_span(x)} elements, needs at least {(rows - 1) * ldx + cols}")
+    if n and span < (rows - 1) * ldx + cols:
+        raise ValueError(f"x: {span} elements, needs at least {(rows - 1) * ldx + cols}")
     rg, cg = _groups(rows), _groups(cols)
-    if out_row is not None or scale_row is not None:
-        _buf(out_row, "out_row", n, _BYTE1, nullable=False)
-        _buf(scale_row, "scale_row", rows * cg, _F32, nullable=False)
-    if out_col is not None or scale_col is not None:
-        _buf(out_col, "out_col", n, _BYTE1, nullable=False)
-        _buf(scale_col, "scale_col", rg * cols, _F32, nullable=False)
-    if out_tile is not None or scale_tile is not None:
-        _buf(out_tile, "out_tile", n, _BYTE1, nullable=False)
-        _buf(scale_tile, "scale_tile", rg * cg, _F32, nullable=False)
-    st = _lib.fp8_quantize_block(_ptr(x), in_type, rows, cols, ldx, fmt, margin, _ptr(out_row),
-                                 _ptr(scale_row), _ptr(out_col), _ptr(scale_col),
-                                 _ptr(out_tile), _ptr(scale_tile), _stream(stream))
-    _check(st, "fp8_quantize_block")
-
-
-def _span(x: torch.Tensor) -> int:
-    """Elements from a tensor's first to its last, both counted."""
-    if x.is_contiguous():
-        return x.numel()
-    return (x.shape[0] - 1) * x.stride(0) + x.shape[1]
+    for kind, codes, steps in (("row", out_row, scale_row), ("col", out_col, scale_col),
+                               ("tile", out_tile, scale_tile)):
+        if (codes is None) != (steps is None):
+            raise ValueError(f"{'out' if codes is None else 'scale'}_{kind}: required (codes and "
+                             "steps go together)")
+    at = _addresses((out_row, "out_row", n, _BYTE1), (scale_row, "scale_row", rows * cg, _F32),
+                    (out_col, "out_col", n, _BYTE1), (scale_col, "scale_col", rg * cols, _F32),
+                    (out_tile, "out_tile", n, _BYTE1),
+                    (scale_tile, "scale_tile", rg * cg, _F32))
+    st = _lib.fp8_quantize_block(_ptr(x), in_type, rows, cols, ldx, fmt, margin, *at,
+                                 _stream(stream))
+    if st:
+        _check(st, "fp8_quantize_block")
 
 
 def fp8_mm_block_workspace(m: int, n: int, k: int) -> int:
@@ -676,26 +691,25 @@ def fp8_mm_block(a: torch.Tensor, b: torch.Tensor, fmt_a: int, fmt_b: int, trans
                  workspace: torch.Tensor | None = None, stream=None) -> None:
     """Product of operands with a step for each group of 128 k per row /
     column (GROUP_LINE) or per 128 x 128 tile (GROUP_TILE); see fp8lin.h."""
-    m, n, k = int(m), int(n), int(k)
     if m < 0 or n < 0 or k < 0:
         raise ValueError("fp8_mm_block: negative size")
     if group_a not in (GROUP_LINE, GROUP_TILE) or group_b not in (GROUP_LINE, GROUP_TILE):
         raise ValueError(f"fp8_mm_block: bad grouping {group_a}, {group_b}")
     kg = _groups(k)
-    _buf(a, "a", _extent(k, m, lda, 1, 0) if trans_a else _extent(m, k, lda, 1, 0), _BYTE1,
-         nullable=False)
-    _buf(b, "b", _extent(n, k, ldb, 1, 0) if trans_b else _extent(k, n, ldb, 1, 0), _BYTE1,
-         nullable=False)
-    _buf(scale_a, "scale_a", kg * (_groups(m) if group_a else m), _F32, nullable=False)
-    _buf(scale_b, "scale_b", kg * (_groups(n) if group_b else n), _F32, nullable=False)
-    _buf(bias, "bias", n, _BF16)
-    _buf(out, "out", m * n, _BF16, nullable=False)
-    st = _lib.fp8_mm_block(_ptr(a), _ptr(b), fmt_a, fmt_b, trans_a, trans_b, m, n, k, lda, ldb,
-                           _ptr(scale_a), group_a, _ptr(scale_b), group_b, _ptr(bias),
-                           _ptr(out), _ptr(workspace),
+    if a is None or b is None or scale_a is None or scale_b is None or out is None:
+        raise ValueError("fp8_mm_block: a, b, scale_a, scale_b and out are required")
+    pa, pb, psa, psb, pbias, pout = _addresses(
+        (a, "a", _extent(k, m, lda, 1, 0) if trans_a else _extent(m, k, lda, 1, 0), _BYTE1),
+        (b, "b", _extent(n, k, ldb, 1, 0) if trans_b else _extent(k, n, ldb, 1, 0), _BYTE1),
+        (scale_a, "scale_a", kg * (_groups(m) if group_a else m), _F32),
+        (scale_b, "scale_b", kg * (_groups(n) if group_b else n), _F32),
+        (bias, "bias", n, _BF16), (out, "out", m * n, _BF16))
+    st = _lib.fp8_mm_block(pa, pb, fmt_a, fmt_b, trans_a, trans_b, m, n, k, lda, ldb, psa, group_a,
+                           psb, group_b, pbias, pout, _ptr(workspace),
                            0 if workspace is None else _ws_bytes(workspace, "workspace"),
                            _stream(stream))
-    _check(st, "fp8_mm_block")
+    if st:
+        _check(st, "fp8_mm_block")
 
 
 def fp8_linear_block_saved(M: int, N: int, K: int, want_dx: bool, want_dw: bool) -> int:
@@ -796,17 +810,16 @@ def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, s13: torch
     experts with tile-scaled fp8 weights, weighted sum; see fp8lin.h."""
     if min(tokens, experts, top_k, dim, hidden) < 0:
         raise ValueError("fp8_moe: negative size")
-    _buf(x, "x", tokens * dim, _BF16, nullable=False)
-    _buf(router, "router", experts * dim, _BF16, nullable=False)
-    _buf(w13, "w13", experts * 2 * hidden * dim, _BYTE1, nullable=False)
-    _buf(s13, "s13", experts * _groups(2 * hidden) * _groups(dim), _F32, nullable=False)
-    _buf(w2, "w2", experts * dim * hidden, _BYTE1, nullable=False)
-    _buf(s2, "s2", experts * _groups(dim) * _groups(hidden), _F32, nullable=False)
-    _buf(out, "out", tokens * dim, _BF16, nullable=False)
-    _buf(ids, "ids", tokens * top_k, (torch.int32,))
-    _buf(weights, "weights", tokens * top_k, _F32)
-    st = _lib.fp8_moe(_ptr(x), _ptr(router), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), tokens,
-                      experts, top_k, dim, hidden, fmt, int(bool(renormalize)), _ptr(workspace),
-                      _ws_bytes(workspace, "workspace"), _ptr(out), _ptr(ids), _ptr(weights),
-                      _stream(stream))
-    _check(st, "fp8_moe")
+    px, pr, pw13, ps13, pw2, ps2, pout, pids, pweights = _addresses(
+        (x, "x", tokens * dim, _BF16), (router, "router", experts * dim, _BF16),
+        (w13, "w13", experts * 2 * hidden * dim, _BYTE1),
+        (s13, "s13", experts * _groups(2 * hidden) * _groups(dim), _F32),
+        (w2, "w2", experts * dim * hidden, _BYTE1),
+        (s2, "s2", experts * _groups(dim) * _groups(hidden), _F32),
+        (out, "out", tokens * dim, _BF16), (ids, "ids", tokens * top_k, (torch.int32,)),
+        (weights, "weights", tokens * top_k, _F32))
+    st = _lib.fp8_moe(px, pr, pw13, ps13, pw2, ps2, tokens, experts, top_k, dim, hidden, fmt,
+                      int(bool(renormalize)), _ptr(workspace), _ws_bytes(workspace, "workspace"),
+                      pout, pids, pweights, _stream(stream))
+    if st:
+        _check(st, "fp8_moe")
