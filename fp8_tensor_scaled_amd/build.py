@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libfp8lin.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_tiled.hip", "gemm_skinny.hip",
            "block_api.hip", "block_quant.hip", "block_gemm.hip",
            "block_gemm_nt.hip", "block_gemm_nn.hip", "block_gemm_tn.hip",
-           "block_gemm_pair.hip", "moe.hip"]
+           "block_gemm_pair.hip",
+           "block_gemm_skinny.hip", "moe.hip"]
 # the benchmark's ceiling kernels, a library of their own that only bench.py loads
 BENCH_LIB = os.path.join(HERE, "libfp8bench.so")
 BENCH_SOURCES = ["bench_ref.hip"]

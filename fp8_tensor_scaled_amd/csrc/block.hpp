@@ -50,9 +50,13 @@ struct BlockGemmLaunch {
     BlockScale sa, sb;
     const uint16_t* bias = nullptr;
     uint16_t* out = nullptr;
-    void* ws = nullptr;  // block_gemm_workspace bytes, or null: no k split
+    // For a split along k: a counter per tile (zero between calls) and
+    // block_gemm_partials bytes for the shares' sums; null: no split.
+    uint32_t* counters = nullptr;
+    float* part = nullptr;
 };
-size_t block_gemm_workspace(int64_t m, int64_t n, int64_t k);
+constexpr size_t kSplitCounterBytes = 4 * 256;  // at most so many tiles are split
+size_t block_gemm_partials(int64_t m, int64_t n, int64_t k);  // 0: no split
 hipError_t launch_block_gemm(const BlockGemmLaunch& g, hipStream_t stream);
 // A linear backward's dX (NN) and dW (TN) and, with cf.db, the last pass of
 // its bias gradient: one launch where the tiled kernels take both.

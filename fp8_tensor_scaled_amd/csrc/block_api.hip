@@ -78,7 +78,8 @@ fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, i
 
 size_t fp8_mm_block_workspace(int64_t m, int64_t n, int64_t k) {
     if (m < 1 || n < 1 || k < 1) return 0;
-    return fp8lin::block_gemm_workspace(m, n, k);
+    const size_t part = fp8lin::block_gemm_partials(m, n, k);
+    return part ? fp8lin::kSplitCounterBytes + part : 0;
 }
 
 }  // extern "C"
@@ -136,7 +137,7 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
         return fail(FP8_EINVAL, "%s: out or bias is not aligned to its elements", who);
     if (((uintptr_t)scale_a | (uintptr_t)scale_b) & 3)
         return fail(FP8_EINVAL, "%s: a scale is not aligned to its elements", who);
-    const size_t need = fp8lin::block_gemm_workspace(m, n, k);
+    const size_t need = fp8_mm_block_workspace(m, n, k);
     if (workspace) {
         if (workspace_bytes < need)
             return fail(FP8_EINVAL, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
@@ -161,7 +162,11 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
     g.sb = scale_of(scale_b, group_b, trans_b != 0, n, k);
     g.bias = bias;
     g.out = out;
-    g.ws = need ? workspace : nullptr;
+    if (need && workspace) {
+        g.counters = static_cast<uint32_t*>(workspace);
+        g.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                          fp8lin::kSplitCounterBytes);
+    }
     hipError_t e = fp8lin::launch_block_gemm(g, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "block gemm launch");
 }

@@ -218,7 +218,30 @@ hipError_t launch_general(const BlockGemmLaunch& g, hipStream_t stream) {
 
 }  // namespace
 
-size_t block_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
+// Shares of a tile along k.  A group of k takes a 64 x 64 tile's workgroup
+// about 0.27 us (a chain of LDS reads, matrix instructions and a barrier); joining s
+// shares measured 2.5 us + 0.35 us s.  The cheapest number that gives each
+// CU at most one workgroup.
+int block_gemm_splits(int64_t m, int64_t n, int64_t k) {
+    const double all = (double)((m + 63) / 64) * (double)((n + 63) / 64);
+    if (all > 128) return 1;
+    const int tiles = (int)all;
+    const int64_t groups = groups_of(k);
+    int64_t best = 1, cost = 27 * groups;
+    for (int64_t s = 2; s <= 16 && s * tiles <= 256; ++s) {
+        const int64_t per = (groups + s - 1) / s;
+        if ((groups + per - 1) / per != s) continue;  // a share would be empty
+        const int64_t c = 27 * per + 250 + 35 * s;
+        if (c < cost) cost = c, best = s;
+    }
+    return (int)best;
+}
+
+size_t block_gemm_partials(int64_t m, int64_t n, int64_t k) {
+    const int s = block_gemm_splits(m, n, k);
+    if (s == 1) return 0;
+    return (size_t)s * ((m + 63) / 64) * ((n + 63) / 64) * 64 * 64 * sizeof(float);
+}
 
 // What the tiled kernels take: 16-byte aligned operands and leading
 // dimensions, whole 16-byte pieces along the contiguous dimension, operands
@@ -233,17 +256,28 @@ static bool tiled_supported(const BlockGemmLaunch& g) {
     if ((double)(g.trans_a ? g.k : g.m) * (double)g.lda >= lim) return false;
     if ((double)(g.trans_b ? g.n : g.k) * (double)g.ldb >= lim) return false;
     if ((double)g.sa.sk >= lim / 4 || (double)g.sb.sk >= lim / 4) return false;
-    return (double)((g.m + 127) / 128) * (double)((g.n + 127) / 128) < lim;
+    return (double)((g.m + 63) / 64) * (double)((g.n + 63) / 64) < lim;
 }
 
 // A backward's products go in one launch of 128 x 128 tiles up to this many of
 // them (four rounds of the CUs); beyond, each gains more from larger tiles.
 constexpr int kPairTiles = 1024;
 
+// Below this many 128 x 128 tiles, 64 x 64 ones, which spread over more CUs
+// (us, 64 x 64 / 128 x 128: 1024^3 NT, 64 tiles of 128 x 128, 5.7 / 8.0;
+// 1024 x 1536 x 2048, 96 tiles, NT 10.6 / 12.3, TN 14.3 / 14.2; 1920 x 2048 x
+// 1024, 240 tiles, NT 13.0 / 10.1, TN 16.3 / 10.7).
+constexpr int kFewTiles = 128;
+
+// The 128 x 256 and 256 x 128 tiles cost about 675 / 475 of a 128 x 128 one's
+// time; every configuration runs one workgroup per CU, so a launch costs
+// rounds of 256 tiles times that (us, half / 128 x 128: 2048^3 NT 17.4 / 15.2;
+// 2048 x 4096 x 1024 NT 14.9 / 18.3; 3008 x 3008 x 1024 TN 26.4 / 27.9;
+// 4096 x 1024 x 2048 TN 21.3 / 16.3).
 static BlockCfg tile_cfg(const BlockGemmLaunch& g) {
-    auto rounds = [&](int bm, int bn) {
-        return (((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn) + 255) / 256;
-    };
+    auto tiles = [&](int bm, int bn) { return ((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
+    auto rounds = [&](int bm, int bn) { return (tiles(bm, bn) + 255) / 256; };
+    if (tiles(128, 128) < kFewTiles) return BlockCfg::kSmall;
     const BlockCfg half = g.n >= g.m ? BlockCfg::kWide : BlockCfg::kTall;
     const int64_t half_rounds = g.n >= g.m ? rounds(128, 256) : rounds(256, 128);
     return half_rounds * 675 <= rounds(128, 128) * 475 ? half : BlockCfg::kMid;
@@ -266,6 +300,12 @@ hipError_t launch_block_gemm_pair(const BlockGemmLaunch& dx, const BlockGemmLaun
 
 hipError_t launch_block_gemm(const BlockGemmLaunch& g, hipStream_t stream) {
     if (tiled_supported(g)) {
+        // Short A against a weight: the bandwidth-shaped kernel, but for a long k
+        // over few columns, where the split one has more of the chip to itself
+        // (16 x 128 x 16384: 11.6 us split, 22.5; 16 x 1024 x 4096: 8.0 against 9.2).
+        if (!g.trans_a && g.trans_b && g.m <= 64 &&
+            (g.k <= 64 * kGroup || !g.part || block_gemm_splits(g.m, g.n, g.k) == 1))
+            return launch_block_skinny(g, stream);
         const bool bvec = g.sb.shift == 0;
         const BlockCfg c = tile_cfg(g);
         if (g.trans_a) return launch_block_tn(g, bvec, c, stream);

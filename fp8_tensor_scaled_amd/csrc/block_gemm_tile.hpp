@@ -43,6 +43,11 @@ struct BlockTileParams {
     int tiles_m, tiles_n, group_m;
     int vec_out16;  // whole 16-byte chunks of output rows (and bias), aligned
     int xcd_remap;
+    // Split along k: `splits` workgroups share a tile, each taking
+    // groups_per groups; partial sums and a counter per tile in a workspace.
+    int splits, groups_per;
+    float* part;
+    uint32_t* counters;
 };
 
 // One global -> LDS load of a dword per lane: lane l's goes to LDS at M0 + 4 l.
@@ -68,8 +73,12 @@ struct BlockTile {
     static_assert(kLds <= 160 * 1024, "LDS");
 };
 
-// One output tile: workgroup `bid` of a grid of `wgs` over problem p.
-template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+// One output tile: workgroup `bid` of a grid of `wgs` over problem p.  With
+// SPLIT it is one share of a tile along k: the sums go to the workspace at
+// device scope, and the workgroup that brings the last share adds them all, in
+// the shares' order, and writes the tile.
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST,
+          bool SPLIT = false>
 __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bid, int wgs,
                                                 uint8_t* smem) {
     using BT = BlockTile<BVEC, BM, BN, WM, WN, ST>;
@@ -91,6 +100,12 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     const int wm = wave / WN, wn = wave % WN;
 
     if (p.xcd_remap) bid = (bid & 7) * (wgs >> 3) + (bid >> 3);
+    int share = 0;
+    if constexpr (SPLIT) {
+        const int tiles = p.tiles_m * p.tiles_n;
+        share = bid / tiles;
+        bid -= share * tiles;
+    }
     const int per_group = p.group_m * p.tiles_n;
     const int first_m = (bid / per_group) * p.group_m;
     const int gsz = p.tiles_m - first_m < p.group_m ? p.tiles_m - first_m : p.group_m;
@@ -98,10 +113,13 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane((first_m + r % gsz) * BM);
     const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane((r / gsz) * BN);
 
-    const v4i ra = make_rsrc(p.a + (AMN ? m0 : m0 * p.lda));
-    const v4i rb = make_rsrc(p.b + (BMN ? n0 : n0 * p.ldb));
+    const int g0 = SPLIT ? share * p.groups_per : 0;  // first group of k
+    const int64_t k0 = (int64_t)g0 * BK;
+    const v4i ra = make_rsrc(p.a + (AMN ? m0 + k0 * p.lda : m0 * p.lda + k0));
+    const v4i rb = make_rsrc(p.b + (BMN ? n0 + k0 * p.ldb : n0 * p.ldb + k0));
     const uint32_t lda = (uint32_t)p.lda, ldb = (uint32_t)p.ldb;
-    const int kdim = (int)p.k;
+    const int left = (int)(p.k - k0);
+    const int kdim = SPLIT && left > p.groups_per * BK ? p.groups_per * BK : left;
     const int nk = (kdim + BK - 1) / BK;
     const int64_t arows = p.m - m0, brows = p.n - n0;
     const bool afull = arows >= BM, bfull = brows >= BN;
@@ -124,7 +142,7 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
             i = j < p.n ? j : p.n - 1;
         }
         const BlockScale& s = is_b ? p.sb : p.sa;
-        step_at = reinterpret_cast<uint64_t>(s.s + (i >> s.shift) * s.si);
+        step_at = reinterpret_cast<uint64_t>(s.s + (i >> s.shift) * s.si + g0 * s.sk);
         step_k = (uint32_t)(s.sk * 4);
     }
 
@@ -219,9 +237,10 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
             const int i = t % FM, j = t / FM;
             if constexpr (H == 0) {
                 const v16f zero = {0};
-                static_assert(kMF > 1, "the last tile's registers outlive the first's start");
+                // (with one tile per wave its registers are needed at once)
+                if (!BVEC && kMF == 1) fold(acc[0][0], part[0], prev_a, nullptr);
                 part[t] = mfma_ba<FA, FB>(bf[0][j], af[0][i], zero);
-                if (!BVEC && t == 0)
+                if (!BVEC && kMF > 1 && t == 0)
                     fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
             } else {
                 part[t] = mfma_ba<FA, FB>(bf[1][j], af[1][i], part[t]);
@@ -291,6 +310,66 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     }
     if constexpr (!BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
     wait_vmcnt<0>();  // the prefetches past the end
+
+    if constexpr (SPLIT) {
+        // a lane's sums as pairs: pair q of lane l of a tile is 64 q + l
+        const int tiles = p.tiles_m * p.tiles_n;
+        auto at = [&](int sh, int t) {
+            return reinterpret_cast<uint64_t*>(p.part) +
+                   (((int64_t)sh * tiles + bid) * NW + wave) * (kMF * 512) + t * 512 + lane;
+        };
+#pragma unroll
+        for (int t = 0; t < kMF; ++t)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const v16f& v = acc[t % FM][t / FM];
+                const uint64_t pair = __float_as_uint(v[2 * q]) |
+                                      (uint64_t)__float_as_uint(v[2 * q + 1]) << 32;
+                __hip_atomic_store(at(share, t) + 64 * q, pair, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            }
+        wait_vmcnt<0>();  // the stores have reached device scope
+        barrier();
+        if (tid == 0) {
+            const uint32_t seen = __hip_atomic_fetch_add(p.counters + bid, 1u, __ATOMIC_RELAXED,
+                                                         __HIP_MEMORY_SCOPE_AGENT);
+            if (seen == (uint32_t)p.splits - 1)
+                __hip_atomic_store(p.counters + bid, 0u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            *reinterpret_cast<uint32_t*>(smem) = seen == (uint32_t)p.splits - 1;
+        }
+        __syncthreads();
+        if (*reinterpret_cast<volatile uint32_t*>(smem) == 0) return;
+#pragma unroll
+        for (int t = 0; t < kMF; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[t % FM][t / FM][e] = 0.0f;
+        // four shares' loads at a time: each takes about a microsecond
+        constexpr int kAhead = 4;
+        for (int s0 = 0; s0 < p.splits; s0 += kAhead)
+#pragma unroll
+            for (int t = 0; t < kMF; ++t) {
+                uint64_t pair[kAhead][8];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        pair[i][q] = __hip_atomic_load(
+                            at(s0 + i < p.splits ? s0 + i : s0, t) + 64 * q, __ATOMIC_RELAXED,
+                            __HIP_MEMORY_SCOPE_AGENT);
+                v16f& v = acc[t % FM][t / FM];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (s0 + i >= p.splits) break;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        v[2 * q] += __uint_as_float((uint32_t)pair[i][q]);
+                        v[2 * q + 1] += __uint_as_float((uint32_t)(pair[i][q] >> 32));
+                    }
+                }
+            }
+        barrier();  // the flag is read before the tile is staged over it
+    }
 
     // acc[i][j][e] is row m0 + wm*TM + 32i + lane%32, column
     // n0 + wn*TN + 32j + 8*(e/4) + 4*(lane/32) + e%4.
@@ -362,7 +441,19 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTilePar
     block_gemm_tile<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST>(p, blockIdx.x, gridDim.x, smem);
 }
 
-enum class BlockCfg { kWide, kTall, kMid };
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_split_kernel(BlockTileParams p) {
+    __shared__ __attribute__((aligned(1024)))
+    uint8_t smem[BlockTile<BVEC, BM, BN, WM, WN, ST>::kLds];
+    block_gemm_tile<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST, true>(p, blockIdx.x, gridDim.x,
+                                                                     smem);
+}
+
+// Tiles: kWide 128 x 256, kTall 256 x 128, kMid 128 x 128, kSmall 64 x 64.
+enum class BlockCfg { kWide, kTall, kMid, kSmall };
+// How a product of 64 x 64 tiles is split along k: 1 for not at all.
+int block_gemm_splits(int64_t m, int64_t n, int64_t k);
+hipError_t launch_block_skinny(const BlockGemmLaunch& g, hipStream_t stream);  // NT, m <= 64
 hipError_t launch_block_nt(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
 hipError_t launch_block_nn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
 hipError_t launch_block_tn(const BlockGemmLaunch& g, bool bvec, BlockCfg c, hipStream_t stream);
@@ -400,8 +491,25 @@ hipError_t launch_block_tile(const BlockGemmLaunch& g, hipStream_t stream) {
 }
 
 template <int FA, int FB, bool AMN, bool BMN, bool BVEC>
+hipError_t launch_block_small(const BlockGemmLaunch& g, hipStream_t stream) {
+    const int splits = g.part ? block_gemm_splits(g.m, g.n, g.k) : 1;
+    if (splits == 1) return launch_block_tile<FA, FB, AMN, BMN, BVEC, 64, 64, 2, 2, 4>(g, stream);
+    BlockTileParams p = block_tile_params<64, 64>(g);
+    const int tiles = p.tiles_m * p.tiles_n;
+    p.splits = splits;
+    p.groups_per = (int)((groups_of(g.k) + splits - 1) / splits);
+    p.part = g.part;
+    p.counters = g.counters;
+    p.xcd_remap = tiles * splits % 8 == 0;
+    hipLaunchKernelGGL((block_gemm_split_kernel<FA, FB, AMN, BMN, BVEC, 64, 64, 2, 2, 4>),
+                       dim3((unsigned)(tiles * splits)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int FA, int FB, bool AMN, bool BMN, bool BVEC>
 hipError_t launch_block_cfg(const BlockGemmLaunch& g, BlockCfg c, hipStream_t stream) {
     switch (c) {
+        case BlockCfg::kSmall: return launch_block_small<FA, FB, AMN, BMN, BVEC>(g, stream);
         case BlockCfg::kWide:
             return launch_block_tile<FA, FB, AMN, BMN, BVEC, 128, 256, 2, 4, 3>(g, stream);
         case BlockCfg::kTall:
