@@ -18,8 +18,8 @@ template <int FG, int FO>
 __global__ __launch_bounds__(kThreads, 1) void block_gemm_pair_kernel(BlockTileParams dx,
                                                                      BlockTileParams dw, int n0,
                                                                      int n1, ColsumFinalJob cf) {
-    constexpr int kLds0 = BlockTile<false, kS, kS, 4, 2, kStages>::kLds;
-    constexpr int kLds1 = BlockTile<true, kS, kS, 4, 2, kStages>::kLds;
+    constexpr int kLds0 = BlockTile<false, false, kS, kS, 4, 2, kStages>::kLds;
+    constexpr int kLds1 = BlockTile<true, true, kS, kS, 4, 2, kStages>::kLds;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds0 > kLds1 ? kLds0 : kLds1];
     const int b = blockIdx.x;
     if (b < n0)

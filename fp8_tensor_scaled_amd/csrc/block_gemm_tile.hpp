@@ -19,10 +19,11 @@
 //    values of a tile belong to one row of A: with one step per 128 x 128
 //    tile of B the factor is one number per lane and tile.  With a step per
 //    column (BVEC) each value has a factor of its own: twice the vector work.
-//  * The steps of a stage come with its operands, one load into LDS per
-//    wave: entry e < BM is row e's step, the others B's columns' (or its
-//    tiles').  Read by gathers in every wave they would be fetched WN
-//    times, from 32 lines each time.
+//  * The steps come into LDS with the operands.  Where both operands' lie
+//    along k (A's rows, B's tiles) they come for ST stages at a time, with
+//    the first of them (CHUNK): a row's next ones are in the same line, and
+//    fetching it for each stage cost 4096^3 NT 4 us and 2048 x 1024 x 4096 NN
+//    3.8 of 21.7.  Otherwise each stage brings its own, a line for every 32.
 
 #pragma once
 
@@ -61,15 +62,20 @@ __device__ __forceinline__ v16f mfma_ba(const v8i& b, const v8i& a, v16f acc) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, FB, FA, 0, 0, 0, 0);
 }
 
-template <bool BVEC, int BM, int BN, int WM, int WN, int ST>
+template <bool AMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
 struct BlockTile {
     static constexpr int NW = WM * WN;
     static constexpr int kStage = (BM + BN) * kGroup;  // operand bytes of a stage
     static constexpr int kNB = BVEC ? BN : (BN + kGroup - 1) / kGroup;  // B's steps
-    static constexpr int kPer = (BM + kNB + NW - 1) / NW;  // steps each wave loads
-    static_assert(kPer <= 64, "one step per lane");
-    static constexpr int kSteps = (kPer * NW + 31) / 32 * 32;  // floats per stage
-    static constexpr int kLds = ST * (kStage + 4 * kSteps);
+    static constexpr bool CHUNK = !AMN && !BVEC;
+    // steps of a load (a stage, or ST of them), entries line * D + group
+    static constexpr int D = CHUNK ? ST : 1;
+    static constexpr int kEntries = (BM + kNB) * D;
+    static constexpr int kPer = (kEntries + NW - 1) / NW;  // of each wave
+    static constexpr int kStepLoads = (kPer + 63) / 64;    // a step per lane and load
+    static constexpr int kSteps = (kPer * NW + 31) / 32 * 32;  // floats per slot
+    static constexpr int kStepSlots = CHUNK ? 2 : ST;
+    static constexpr int kLds = ST * kStage + kStepSlots * 4 * kSteps;
     static_assert(kLds <= 160 * 1024, "LDS");
 };
 
@@ -81,7 +87,7 @@ template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM,
           bool SPLIT = false>
 __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bid, int wgs,
                                                 uint8_t* smem) {
-    using BT = BlockTile<BVEC, BM, BN, WM, WN, ST>;
+    using BT = BlockTile<AMN, BVEC, BM, BN, WM, WN, ST>;
     constexpr int NW = BT::NW, BK = kGroup, kStage = BT::kStage, kPer = BT::kPer;
     constexpr int kStageA = BM * BK;
     constexpr int TM = BM / WM, TN = BN / WN;
@@ -90,8 +96,14 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     using OA = Operand<AMN, BM, NW, BK>;
     using OB = Operand<BMN, BN, NW, BK>;
     constexpr int kPA = OA::kPerWave, kPB = OB::kPerWave;
-    constexpr int kLoads = kPA + kPB + 1;  // loads per wave and stage, the steps' last
-    static_assert(ST >= 2 && kLoads * (ST - 1) < 64, "vmcnt range");
+    // loads per wave and stage: operands, and steps with every stage or with
+    // those of ring slot 0
+    constexpr int kOps = kPA + kPB;
+    constexpr int kStepLoads = BT::kStepLoads;
+    constexpr bool CHUNK = BT::CHUNK;
+    constexpr int kLoads = CHUNK ? kOps : kOps + kStepLoads;
+    auto loads_of = [](int slot) constexpr { return CHUNK && slot == 0 ? kOps + kStepLoads : kLoads; };
+    static_assert(ST >= 2 && kLoads * (ST - 1) + kStepLoads < 64, "vmcnt range");
     uint8_t* steps = smem + ST * kStage;
 
     const int tid = threadIdx.x;
@@ -126,26 +138,31 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     const uint32_t abase = OA::init(lda, arows, wave, lane);
     const uint32_t bbase = OB::init(ldb, brows, wave, lane);
 
-    // This lane's step: its address at group 0 and the bytes to the next
-    // group.  Rows (columns) past the matrix read its last one's.
-    uint64_t step_at;
-    uint32_t step_k;
-    {
-        int e = wave * kPer + (lane < kPer ? lane : kPer - 1);
-        if (e >= BM + BT::kNB) e = BM + BT::kNB - 1;
-        const bool is_b = e >= BM;
+    // This lane's steps: address at group 0 (with CHUNK, at its group of a
+    // chunk) and the bytes to the next group.  Lines past the matrix read its
+    // last one's.
+    uint64_t step_at[kStepLoads];
+    uint32_t step_k[kStepLoads];
+    int step_g[kStepLoads];
+#pragma unroll
+    for (int x = 0; x < kStepLoads; ++x) {
+        const int in = 64 * x + lane < kPer ? 64 * x + lane : kPer - 1;
+        int e = wave * kPer + in;
+        if (e >= BT::kEntries) e = BT::kEntries - 1;
+        const int line = e / BT::D;
+        step_g[x] = e % BT::D;
+        const bool is_b = line >= BM;
         int64_t i;
         if (!is_b) {
-            i = m0 + e < p.m ? m0 + e : p.m - 1;
+            i = m0 + line < p.m ? m0 + line : p.m - 1;
         } else {
-            const int64_t j = BVEC ? n0 + (e - BM) : (n0 / kGroup + (e - BM)) * kGroup;
+            const int64_t j = BVEC ? n0 + (line - BM) : (n0 / kGroup + (line - BM)) * kGroup;
             i = j < p.n ? j : p.n - 1;
         }
         const BlockScale& s = is_b ? p.sb : p.sa;
-        step_at = reinterpret_cast<uint64_t>(s.s + (i >> s.shift) * s.si + g0 * s.sk);
-        step_k = (uint32_t)(s.sk * 4);
+        step_at[x] = reinterpret_cast<uint64_t>(s.s + (i >> s.shift) * s.si + g0 * s.sk);
+        step_k[x] = (uint32_t)(s.sk * 4);
     }
-
     // Load x of the stage at group kg into ring slot s.
     auto load = [&](int x, int s, int kg) __attribute__((always_inline)) {
         uint8_t* dst = smem + s * kStage;
@@ -156,10 +173,13 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
             dma16(rb, OB::lds_of(dst + kStageA, x - kPA, wave),
                   OB::off_of(bbase, ldb, kg * BK, kdim, bfull, brows, x - kPA, wave, lane));
         } else {
-            const int g = kg < nk ? kg : nk - 1;  // past the end: any group
-            if (lane < kPer)
-                dma4(step_at + (uint64_t)g * step_k,
-                     lds_addr(steps + 4 * (s * BT::kSteps + wave * kPer)));
+            const int y = x - kPA - kPB;
+            const int slot = CHUNK ? kg / ST & 1 : s;
+            int g = kg + step_g[y];
+            if (g >= nk) g = nk - 1;  // past the end: any group
+            if (64 * y + lane < kPer)
+                dma4(step_at[y] + (uint64_t)g * step_k[y],
+                     lds_addr(steps + 4 * (slot * BT::kSteps + wave * kPer + 64 * y)));
         }
     };
 
@@ -191,8 +211,9 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     v4f sb[BVEC ? FN : 1][4];
     typedef const __attribute__((address_space(3))) float lds_f32;
     typedef const __attribute__((address_space(3))) v4f lds_v4f;
-    auto read_steps = [&](int s) __attribute__((always_inline)) {
-        uint8_t* at = steps + 4 * s * BT::kSteps;
+    // ring slot s of the turn `turn` of the ring
+    auto read_steps = [&](int s, int turn) __attribute__((always_inline)) {
+        uint8_t* at = steps + 4 * (CHUNK ? (turn & 1) * BT::kSteps + s : s * BT::kSteps);
         if constexpr (BVEC) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
@@ -204,10 +225,10 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
 #pragma unroll
         for (int i = 0; i < FM; ++i)
             sa[i] = *reinterpret_cast<lds_f32*>(
-                (lds_void*)(at + 4 * (wm * TM + 32 * i + (lane & 31))));
+                (lds_void*)(at + 4 * BT::D * (wm * TM + 32 * i + (lane & 31))));
         if constexpr (!BVEC) {
             const float b = *reinterpret_cast<lds_f32*>(
-                (lds_void*)(at + 4 * (BM + wn * TN / kGroup)));
+                (lds_void*)(at + 4 * BT::D * (BM + wn * TN / kGroup)));
 #pragma unroll
             for (int i = 0; i < FM; ++i) sa[i] *= b;
         }
@@ -274,15 +295,17 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     // slot, the rest in the next stage's first substep.
     constexpr bool kSplit = ST >= 3;
     constexpr int kH = kSplit ? (kLoads + 1) / 2 : kLoads;
+    static_assert(kSplit || !CHUNK, "the steps go with a refill's second part");
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     using IH = std::integral_constant<int, kH>;
     using IL = std::integral_constant<int, kLoads>;
+    using IL0 = std::integral_constant<int, loads_of(0)>;
 
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
 #pragma unroll
-        for (int x = 0; x < kLoads; ++x) load(x, s, s);
+        for (int x = 0; x < loads_of(s); ++x) load(x, s, s);
 #pragma unroll
     for (int x = 0; x < kH; ++x) load(x, ST - 1, ST - 1);
     wait_vmcnt<kLoads * (ST - 2) + kH>();
@@ -293,17 +316,22 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     for (int j = 0; j < FN; ++j)
         bf[0][j] = OB::template frag<0>(smem + kStageA + brow + 32 * j * kRowB, boff[j]);
 
-    for (int t0 = 0; t0 < nk; t0 += ST) {
+    for (int t0 = 0, turn = 0; t0 < nk; t0 += ST, ++turn) {
 #pragma unroll
         for (int s = 0; s < ST; ++s) {
             const int st = t0 + s;
             if (st >= nk) break;
-            read_steps(s);
+            read_steps(s, turn);
             // the rest of the refill that stage st - 1 began
-            constexpr int kPrevSlot = ST - 1;
-            substep(I0{}, s, IH{}, IL{}, (s + kPrevSlot) % ST, st + ST - 1);
-            wait_vmcnt<kLoads * (ST - 2)>();  // this wave's loads of stage st + 1
-            wait_lgkmcnt0();                  // and its reads of this stage
+            const int prev = (s + ST - 1) % ST;
+            if (prev == 0) substep(I0{}, s, IH{}, IL0{}, prev, st + ST - 1);
+            else substep(I0{}, s, IH{}, IL{}, prev, st + ST - 1);
+            // This wave's loads of stage st + 1 (what may be out are those of
+            // the ST - 2 after it, slot 0's steps among them or not), and its
+            // reads of this stage.
+            if (CHUNK && s >= 1 && s <= ST - 2) wait_vmcnt<kLoads * (ST - 2) + kStepLoads>();
+            else wait_vmcnt<kLoads * (ST - 2)>();
+            wait_lgkmcnt0();
             barrier();
             substep(I1{}, (s + 1) % ST, I0{}, IH{}, s, st + ST);
         }
@@ -437,14 +465,14 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
 template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_kernel(BlockTileParams p) {
     __shared__ __attribute__((aligned(1024)))
-    uint8_t smem[BlockTile<BVEC, BM, BN, WM, WN, ST>::kLds];
+    uint8_t smem[BlockTile<AMN, BVEC, BM, BN, WM, WN, ST>::kLds];
     block_gemm_tile<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST>(p, blockIdx.x, gridDim.x, smem);
 }
 
 template <int FA, int FB, bool AMN, bool BMN, bool BVEC, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_split_kernel(BlockTileParams p) {
     __shared__ __attribute__((aligned(1024)))
-    uint8_t smem[BlockTile<BVEC, BM, BN, WM, WN, ST>::kLds];
+    uint8_t smem[BlockTile<AMN, BVEC, BM, BN, WM, WN, ST>::kLds];
     block_gemm_tile<FA, FB, AMN, BMN, BVEC, BM, BN, WM, WN, ST, true>(p, blockIdx.x, gridDim.x,
                                                                      smem);
 }
