@@ -269,18 +269,26 @@ constexpr int kPairTiles = 1024;
 // 1024, 240 tiles, NT 13.0 / 10.1, TN 16.3 / 10.7).
 constexpr int kFewTiles = 128;
 
-// The 128 x 256 and 256 x 128 tiles cost about 675 / 475 of a 128 x 128 one's
-// time; every configuration runs one workgroup per CU, so a launch costs
-// rounds of 256 tiles times that (us, half / 128 x 128: 2048^3 NT 17.4 / 15.2;
-// 2048 x 4096 x 1024 NT 14.9 / 18.3; 3008 x 3008 x 1024 TN 26.4 / 27.9;
-// 4096 x 1024 x 2048 TN 21.3 / 16.3).
+// Every configuration runs one workgroup per CU, so a launch costs rounds of
+// 256 tiles times a tile's time.  Those, in thousandths of a 256 x 256 tile's,
+// with a step per tile of B: half as large 570, 128 x 128 350 (us, 256 x 256 /
+// half / 128 x 128: 4096^3 NT 67 / 75 / 88; 3008 x 3008 x 2048 NT 31.0 / 34.9 /
+// 35.5; 2048 x 4096 x 4096 NT 54.5 / 38.9 / 44.7; 2048^3 NT - / 17.4 / 15.2).
+// With a step per column of B, which the 256 x 256 tile has no registers for, a
+// 128 x 128 one costs 475 / 675 of the half (2048^3 TN 21.2 / 16.5, 3008 x 3008 x
+// 1024 TN 26.4 / 27.9).
 static BlockCfg tile_cfg(const BlockGemmLaunch& g) {
     auto tiles = [&](int bm, int bn) { return ((g.m + bm - 1) / bm) * ((g.n + bn - 1) / bn); };
     auto rounds = [&](int bm, int bn) { return (tiles(bm, bn) + 255) / 256; };
     if (tiles(128, 128) < kFewTiles) return BlockCfg::kSmall;
+    const bool bvec = g.sb.shift == 0;
     const BlockCfg half = g.n >= g.m ? BlockCfg::kWide : BlockCfg::kTall;
-    const int64_t half_rounds = g.n >= g.m ? rounds(128, 256) : rounds(256, 128);
-    return half_rounds * 675 <= rounds(128, 128) * 475 ? half : BlockCfg::kMid;
+    const int64_t half_cost =
+        (g.n >= g.m ? rounds(128, 256) : rounds(256, 128)) * (bvec ? 675 : 570);
+    const int64_t mid_cost = rounds(128, 128) * (bvec ? 475 : 350);
+    if (!bvec && rounds(256, 256) * 1000 <= half_cost && rounds(256, 256) * 1000 <= mid_cost)
+        return BlockCfg::kBig;
+    return half_cost <= mid_cost ? half : BlockCfg::kMid;
 }
 
 hipError_t launch_block_gemm_pair(const BlockGemmLaunch& dx, const BlockGemmLaunch& dw,

@@ -57,6 +57,29 @@ __device__ __forceinline__ void dma4(uint64_t addr, uint32_t lds) {
     asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(addr), "{m0}"(lds));
 }
 
+// Keeps what is computed from x after this point and what x is computed from
+// before it: the order of the matrix and vector instructions below is what
+// bounds the registers, and nothing else would hold it.
+__device__ __forceinline__ void pin(v8i& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void pin(float (&x)[16]) {
+    asm volatile(""
+                 : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]),
+                   "+v"(x[6]), "+v"(x[7]), "+v"(x[8]), "+v"(x[9]), "+v"(x[10]), "+v"(x[11]),
+                   "+v"(x[12]), "+v"(x[13]), "+v"(x[14]), "+v"(x[15]));
+}
+
+template <class T>
+__device__ __forceinline__ T* lds_at(uint32_t address) {
+    return (T*)(uintptr_t)address;
+}
+
+// The same from a descriptor, 32-bit offset per lane and uniform offset.
+__device__ __forceinline__ void dma4_at(const v4i& rsrc, uint32_t lds, uint32_t voff, int soff) {
+    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds));
+}
+
 template <int FA, int FB>
 __device__ __forceinline__ v16f mfma_ba(const v8i& b, const v8i& a, v16f acc) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, FB, FA, 0, 0, 0, 0);
@@ -67,13 +90,14 @@ struct BlockTile {
     static constexpr int NW = WM * WN;
     static constexpr int kStage = (BM + BN) * kGroup;  // operand bytes of a stage
     static constexpr int kNB = BVEC ? BN : (BN + kGroup - 1) / kGroup;  // B's steps
-    static constexpr bool CHUNK = !AMN && !BVEC;
+    static constexpr bool CHUNK = !AMN && !BVEC && ST >= 3;
     // steps of a load (a stage, or ST of them), entries line * D + group
     static constexpr int D = CHUNK ? ST : 1;
     static constexpr int kEntries = (BM + kNB) * D;
     static constexpr int kPer = (kEntries + NW - 1) / NW;  // of each wave
     static constexpr int kStepLoads = (kPer + 63) / 64;    // a step per lane and load
-    static constexpr int kSteps = (kPer * NW + 31) / 32 * 32;  // floats per slot
+    // floats per slot (the large tile's loop lays them out with room between)
+    static constexpr int kSteps = (kPer * NW + 31) / 32 * 32 + (BM * BN == 256 * 256 ? 96 : 0);
     static constexpr int kStepSlots = CHUNK ? 2 : ST;
     static constexpr int kLds = ST * kStage + kStepSlots * 4 * kSteps;
     static_assert(kLds <= 160 * 1024, "LDS");
@@ -92,6 +116,10 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     constexpr int kStageA = BM * BK;
     constexpr int TM = BM / WM, TN = BN / WN;
     constexpr int FM = TM / 32, FN = TN / 32, kMF = FM * FN;
+    // 128 x 64 per wave: partial sums and A's fragments of all its tiles do
+    // not fit the registers beside the sums, so it goes row tile by row tile.
+    constexpr bool BIG = FM == 4 && FN == 2;
+    static_assert(!BIG || (ST == 2 && !BVEC), "the large tile's loop");
     static_assert(TN <= kGroup && kGroup % TN == 0, "a wave's columns share a tile of B");
     using OA = Operand<AMN, BM, NW, BK>;
     using OB = Operand<BMN, BN, NW, BK>;
@@ -183,7 +211,7 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         }
     };
 
-    v8i af[2][FM], bf[2][FN];
+    v8i af[2][BIG ? 1 : FM], bf[2][FN];
     uint32_t aoff[FM], boff[FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i) aoff[i] = OA::frag_off(AMN ? wm * TM + 32 * i : 0, lane);
@@ -198,11 +226,14 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         asm volatile("" ::: "memory");
     };
 
-    v16f acc[FM][FN], part[kMF];
+    constexpr int kParts = BIG ? FN : kMF;
+    // (the sums are plain numbers: only `part` is a matrix register tuple)
+    float acc[FM][FN][16];
+    v16f part[kParts];
 #pragma unroll
     for (int t = 0; t < kMF; ++t)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[t % FM][t / FM][e] = 0.0f, part[t][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) acc[t % FM][t / FM][e] = 0.0f, part[t % kParts][e] = 0.0f;
     // The steps of the stage in work: rows', and with BVEC columns' (16 of
     // each 32-column tile); prev_a: the last tile's of the stage before.
     // With BVEC the last tile is summed in its own stage: carrying its
@@ -233,7 +264,7 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
             for (int i = 0; i < FM; ++i) sa[i] *= b;
         }
     };
-    auto fold = [&](v16f& a, const v16f& pt, float fa, const v4f* fb)
+    auto fold = [&](float (&a)[16], const v16f& pt, float fa, const v4f* fb)
                     __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -242,101 +273,263 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         }
     };
 
-    // Substep H of the stage in slot s: its matrix instructions; between
-    // them the reads of the next substep's fragments (slot ns) and loads
-    // [X0, X1) of the refill of slot rs with group rk.
-    constexpr int kFR = FM + FN, kFRPer = (kFR + kMF - 1) / kMF;
-    auto substep = [&](auto hc, int ns, auto x0c, auto x1c, int rs, int rk)
-                       __attribute__((always_inline)) {
-        constexpr int H = decltype(hc)::value;
-        constexpr int X0 = decltype(x0c)::value, X1 = decltype(x1c)::value;
-        constexpr int kDPer = (X1 - X0 + kMF - 1) / kMF;
-        const uint8_t* la = smem + ns * kStage + arow;
-        const uint8_t* lb = smem + ns * kStage + kStageA + brow;
+    if constexpr (BIG) {
+        // Per row tile i: two matrix instructions of each column tile on the
+        // first 64 k, then two on the second, and behind them the sums:
+        //   M(0,j0)  sum(i-1,j1)  M(0,j1)  M(1,j0)  M(1,j1)  sum(i,j0)
+        // A's fragments of the next row tile replace each half's as soon as
+        // it is used.  The stage ends inside its last row tile: once the
+        // first half's instructions are out, nothing of the slot is left to
+        // read but what has arrived, so the barrier comes there, and the
+        // second half's instructions cover the next stage's first reads.
+        //
+        // 128 sums, 32 partial ones and 48 fragment registers leave about 40
+        // for all else, and a register spilled inside the loop would be read
+        // back behind every load in flight: so the fragments' LDS addresses
+        // are kept per slot and moved to the other one each stage, and the
+        // steps come by 32-bit offsets from descriptors.
+        typedef const __attribute__((address_space(3))) v4i lds_v4i;
+        typedef __attribute__((address_space(3))) v2i lds_v2i;
+        constexpr int kAddrA = AMN ? FM : 4, kAddrB = BMN ? FN : 4;
+        uint32_t fa[kAddrA], fb[kAddrB];
 #pragma unroll
-        for (int t = 0; t < kMF; ++t) {
-            const int i = t % FM, j = t / FM;
-            if constexpr (H == 0) {
-                const v16f zero = {0};
-                // (with one tile per wave its registers are needed at once)
-                if (!BVEC && kMF == 1) fold(acc[0][0], part[0], prev_a, nullptr);
-                part[t] = mfma_ba<FA, FB>(bf[0][j], af[0][i], zero);
-                if (!BVEC && kMF > 1 && t == 0)
-                    fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
+        for (int x = 0; x < kAddrA; ++x)
+            fa[x] = lds_addr(smem) + arow +
+                    (AMN ? aoff[AMN ? x : 0] : aoff[0] ^ (64u * (x / 2) + 16u * (x % 2)));
+#pragma unroll
+        for (int x = 0; x < kAddrB; ++x)
+            fb[x] = lds_addr(smem) + kStageA + brow +
+                    (BMN ? boff[BMN ? x : 0] : boff[0] ^ (64u * (x / 2) + 16u * (x % 2)));
+        auto frag = [&](auto mnc, auto rc, auto hc, const uint32_t* f, int i)
+                        __attribute__((always_inline)) {
+            constexpr int R = decltype(rc)::value, H = decltype(hc)::value;
+            v8i v;
+            if constexpr (!decltype(mnc)::value) {
+                const v4i lo = *lds_at<lds_v4i>(f[2 * H] + 32 * i * BK);
+                const v4i hi = *lds_at<lds_v4i>(f[2 * H + 1] + 32 * i * BK);
+                v[0] = lo[0]; v[1] = lo[1]; v[2] = lo[2]; v[3] = lo[3];
+                v[4] = hi[0]; v[5] = hi[1]; v[6] = hi[2]; v[7] = hi[3];
             } else {
-                part[t] = mfma_ba<FA, FB>(bf[1][j], af[1][i], part[t]);
-                if (t > 0) {
-                    const int u = t - 1;
-                    fold(acc[u % FM][u / FM], part[u], sa[u % FM], sb[BVEC ? u / FM : 0]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v2i t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        lds_at<lds_v2i>(f[i] + (kSub * H + 8 * q) * R));
+                    v[2 * q] = t[0];
+                    v[2 * q + 1] = t[1];
                 }
             }
+            return v;
+        };
+        using TA = std::integral_constant<bool, AMN>;
+        using TB = std::integral_constant<bool, BMN>;
+        using RA = std::integral_constant<int, BM>;
+        using RB = std::integral_constant<int, BN>;
+        using I0 = std::integral_constant<int, 0>;
+        using I1 = std::integral_constant<int, 1>;
+        auto read_a = [&](auto hc, int i) __attribute__((always_inline)) {
+            af[decltype(hc)::value][0] = frag(TA{}, RA{}, hc, fa, i);
+        };
+        auto read_b = [&](auto hc) __attribute__((always_inline)) {
 #pragma unroll
-            for (int q = 0; q < kFRPer; ++q) {
-                const int x = t * kFRPer + q;
-                if (x < FM) af[1 - H][x] = OA::template frag<1 - H>(la + 32 * x * kRowA, aoff[x]);
-                else if (x < kFR)
-                    bf[1 - H][x - FM] =
-                        OB::template frag<1 - H>(lb + 32 * (x - FM) * kRowB, boff[x - FM]);
+            for (int j = 0; j < FN; ++j) bf[decltype(hc)::value][j] = frag(TB{}, RB{}, hc, fb, j);
+        };
+        // Steps: rows 32 wave .. + 63 (half of them the next wave's too), and
+        // by every wave the two of B's tiles, in all 64 lanes: the same values
+        // meet in the same places, and no lane has to be masked.
+        const v4i rsa = make_rsrc(p.sa.s + g0 * p.sa.sk), rsb = make_rsrc(p.sb.s + g0 * p.sb.sk);
+        const int ska = (int)p.sa.sk * 4, skb = (int)p.sb.sk * 4;
+        uint32_t voa, vob;
+        {
+            const int64_t i = m0 + 32 * wave + lane, j = n0 + (lane & 1) * kGroup;
+            voa = (uint32_t)(((i < p.m ? i : p.m - 1) >> p.sa.shift) * p.sa.si * 4);
+            vob = (uint32_t)(((j < p.n ? j : p.n - 1) >> p.sb.shift) * p.sb.si * 4);
+        }
+        constexpr int kStepB = BM + 32, kStepRow = kStepB + 64;  // floats per slot
+        static_assert(2 * kStepRow <= ST * BT::kSteps, "the slots fit");
+        const uint32_t steps_at = lds_addr(steps);
+        constexpr int kBigLoads = kPA + kPB + 2;
+        // load x of the stage at group kg into slot s
+        auto big_load = [&](int x, int s, int kg) __attribute__((always_inline)) {
+            if (x < kPA + kPB) {
+                load(x, s, kg);
+            } else {
+                const int g = kg < nk ? kg : nk - 1;
+                const uint32_t at = steps_at + 4 * s * kStepRow;
+                if (x == kPA + kPB) dma4_at(rsa, at + 128 * wave, voa, g * ska);
+                else dma4_at(rsb, at + 4 * kStepB, vob, g * skb);
             }
+        };
+        auto big_steps = [&](int s) __attribute__((always_inline)) {
+            const uint32_t at = steps_at + 4 * s * kStepRow;
+            const float b = *lds_at<lds_f32>(at + 4 * (kStepB + wn * TN / kGroup));
 #pragma unroll
-            for (int q = 0; q < kDPer; ++q) {
-                const int x = X0 + t * kDPer + q;
-                if (x < X1) load(x, rs, rk);
+            for (int i = 0; i < FM; ++i)
+                sa[i] = *lds_at<lds_f32>(at + 4 * (wm * TM + 32 * i + (lane & 31))) * b;
+        };
+#pragma unroll
+        for (int x = 0; x < kBigLoads; ++x) big_load(x, 0, 0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) big_load(x, 1, 1);
+        wait_vmcnt<2>();
+        barrier();
+        read_a(I0{}, 0);
+        read_b(I0{});
+        read_a(I1{}, 0);
+        read_b(I1{});
+        big_steps(0);
+        const v16f zero = {0};
+        int move = kStage;  // to the other slot
+        for (int st = 0, s = 0; st < nk; ++st, s ^= 1) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                pin(af[0][0]);
+                part[0] = mfma_ba<FA, FB>(bf[0][0], af[0][0], zero);
+                // the row tile before's second sums
+                fold(acc[(i + FM - 1) % FM][1], part[1], i == 0 ? prev_a : sa[(i + FM - 1) % FM],
+                     nullptr);
+                pin(acc[(i + FM - 1) % FM][1]);
+                __builtin_amdgcn_sched_barrier(0);
+                pin(af[0][0]);
+                part[1] = mfma_ba<FA, FB>(bf[0][1], af[0][0], zero);
+                if (i + 1 < FM) {
+                    read_a(I0{}, i + 1);
+                    // the rest of the refill that the stage before began
+                    constexpr int kPerTile = (kBigLoads - 2 + 1) / 2;
+                    if (i < 2) {
+#pragma unroll
+                        for (int x = 2 + i * kPerTile; x < 2 + (i + 1) * kPerTile; ++x)
+                            if (x < kBigLoads) big_load(x, s ^ 1, st + 1);
+                    }
+                } else {
+                    wait_vmcnt<0>();  // this wave's loads of stage st + 1
+                    wait_lgkmcnt0();  // and its reads of this stage
+                    barrier();
+#pragma unroll
+                    for (int x = 0; x < kAddrA; ++x) fa[x] += move;
+#pragma unroll
+                    for (int x = 0; x < kAddrB; ++x) fb[x] += move;
+                    move = -move;
+                    read_a(I0{}, 0);
+                    read_b(I0{});
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                pin(af[1][0]);
+                part[0] = mfma_ba<FA, FB>(bf[1][0], af[1][0], part[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                pin(af[1][0]);
+                part[1] = mfma_ba<FA, FB>(bf[1][1], af[1][0], part[1]);
+                if (i + 1 < FM) {
+                    read_a(I1{}, i + 1);
+                } else {
+                    read_a(I1{}, 0);
+                    read_b(I1{});
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) big_load(x, s, st + ST);
+                }
+                fold(acc[i][0], part[0], sa[i], nullptr);
+                pin(acc[i][0]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            prev_a = sa[FM - 1];
+            big_steps(s ^ 1);
         }
-        if constexpr (H == 1) {
-            if constexpr (BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], sa[FM - 1], sb[FN - 1]);
-            else prev_a = sa[FM - 1];
-        }
-    };
-    // A refill's loads go out over two substeps when the ring has the slack
-    // (three stages or more): the first kH after the barrier that frees the
-    // slot, the rest in the next stage's first substep.
-    constexpr bool kSplit = ST >= 3;
-    constexpr int kH = kSplit ? (kLoads + 1) / 2 : kLoads;
-    static_assert(kSplit || !CHUNK, "the steps go with a refill's second part");
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using IH = std::integral_constant<int, kH>;
-    using IL = std::integral_constant<int, kLoads>;
-    using IL0 = std::integral_constant<int, loads_of(0)>;
+    } else {
+        // Substep H of the stage in slot s: its matrix instructions; between
+        // them the reads of the next substep's fragments (slot ns) and loads
+        // [X0, X1) of the refill of slot rs with group rk.
+        constexpr int kFR = FM + FN, kFRPer = (kFR + kMF - 1) / kMF;
+        auto substep = [&](auto hc, int ns, auto x0c, auto x1c, int rs, int rk)
+                           __attribute__((always_inline)) {
+            constexpr int H = decltype(hc)::value;
+            constexpr int X0 = decltype(x0c)::value, X1 = decltype(x1c)::value;
+            constexpr int kDPer = (X1 - X0 + kMF - 1) / kMF;
+            const uint8_t* la = smem + ns * kStage + arow;
+            const uint8_t* lb = smem + ns * kStage + kStageA + brow;
+#pragma unroll
+            for (int t = 0; t < kMF; ++t) {
+                const int i = t % FM, j = t / FM;
+                if constexpr (H == 0) {
+                    const v16f zero = {0};
+                    // (with one tile per wave its registers are needed at once)
+                    if (!BVEC && kMF == 1) fold(acc[0][0], part[0], prev_a, nullptr);
+                    part[t] = mfma_ba<FA, FB>(bf[0][j], af[0][i], zero);
+                    if (!BVEC && kMF > 1 && t == 0)
+                        fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
+                } else {
+                    part[t] = mfma_ba<FA, FB>(bf[1][j], af[1][i], part[t]);
+                    if (t > 0) {
+                        const int u = t - 1;
+                        fold(acc[u % FM][u / FM], part[u], sa[u % FM], sb[BVEC ? u / FM : 0]);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kFRPer; ++q) {
+                    const int x = t * kFRPer + q;
+                    if (x < FM) af[1 - H][x] = OA::template frag<1 - H>(la + 32 * x * kRowA, aoff[x]);
+                    else if (x < kFR)
+                        bf[1 - H][x - FM] =
+                            OB::template frag<1 - H>(lb + 32 * (x - FM) * kRowB, boff[x - FM]);
+                }
+#pragma unroll
+                for (int q = 0; q < kDPer; ++q) {
+                    const int x = X0 + t * kDPer + q;
+                    if (x < X1) load(x, rs, rk);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (H == 1) {
+                if constexpr (BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], sa[FM - 1], sb[FN - 1]);
+                else prev_a = sa[FM - 1];
+            }
+        };
+        // A refill's loads go out over two substeps when the ring has the slack
+        // (three stages or more): the first kH after the barrier that frees the
+        // slot, the rest in the next stage's first substep.
+        constexpr bool kSplit = ST >= 3;
+        constexpr int kH = kSplit ? (kLoads + 1) / 2 : kLoads;
+        static_assert(kSplit || !CHUNK, "the steps go with a refill's second part");
+        using I0 = std::integral_constant<int, 0>;
+        using I1 = std::integral_constant<int, 1>;
+        using IH = std::integral_constant<int, kH>;
+        using IL = std::integral_constant<int, kLoads>;
+        using IL0 = std::integral_constant<int, loads_of(0)>;
 
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
+        for (int s = 0; s < ST - 1; ++s)
 #pragma unroll
-        for (int x = 0; x < loads_of(s); ++x) load(x, s, s);
+            for (int x = 0; x < loads_of(s); ++x) load(x, s, s);
 #pragma unroll
-    for (int x = 0; x < kH; ++x) load(x, ST - 1, ST - 1);
-    wait_vmcnt<kLoads * (ST - 2) + kH>();
-    barrier();
+        for (int x = 0; x < kH; ++x) load(x, ST - 1, ST - 1);
+        wait_vmcnt<kLoads * (ST - 2) + kH>();
+        barrier();
 #pragma unroll
-    for (int i = 0; i < FM; ++i) af[0][i] = OA::template frag<0>(smem + arow + 32 * i * kRowA, aoff[i]);
+        for (int i = 0; i < FM; ++i) af[0][i] = OA::template frag<0>(smem + arow + 32 * i * kRowA, aoff[i]);
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-        bf[0][j] = OB::template frag<0>(smem + kStageA + brow + 32 * j * kRowB, boff[j]);
+        for (int j = 0; j < FN; ++j)
+            bf[0][j] = OB::template frag<0>(smem + kStageA + brow + 32 * j * kRowB, boff[j]);
 
-    for (int t0 = 0, turn = 0; t0 < nk; t0 += ST, ++turn) {
+        for (int t0 = 0, turn = 0; t0 < nk; t0 += ST, ++turn) {
 #pragma unroll
-        for (int s = 0; s < ST; ++s) {
-            const int st = t0 + s;
-            if (st >= nk) break;
-            read_steps(s, turn);
-            // the rest of the refill that stage st - 1 began
-            const int prev = (s + ST - 1) % ST;
-            if (prev == 0) substep(I0{}, s, IH{}, IL0{}, prev, st + ST - 1);
-            else substep(I0{}, s, IH{}, IL{}, prev, st + ST - 1);
-            // This wave's loads of stage st + 1 (what may be out are those of
-            // the ST - 2 after it, slot 0's steps among them or not), and its
-            // reads of this stage.
-            if (CHUNK && s >= 1 && s <= ST - 2) wait_vmcnt<kLoads * (ST - 2) + kStepLoads>();
-            else wait_vmcnt<kLoads * (ST - 2)>();
-            wait_lgkmcnt0();
-            barrier();
-            substep(I1{}, (s + 1) % ST, I0{}, IH{}, s, st + ST);
+            for (int s = 0; s < ST; ++s) {
+                const int st = t0 + s;
+                if (st >= nk) break;
+                read_steps(s, turn);
+                // the rest of the refill that stage st - 1 began
+                const int prev = (s + ST - 1) % ST;
+                if (prev == 0) substep(I0{}, s, IH{}, IL0{}, prev, st + ST - 1);
+                else substep(I0{}, s, IH{}, IL{}, prev, st + ST - 1);
+                // This wave's loads of stage st + 1 (what may be out are those of
+                // the ST - 2 after it, slot 0's steps among them or not), and its
+                // reads of this stage.
+                if (CHUNK && s >= 1 && s <= ST - 2) wait_vmcnt<kLoads * (ST - 2) + kStepLoads>();
+                else wait_vmcnt<kLoads * (ST - 2)>();
+                wait_lgkmcnt0();
+                barrier();
+                substep(I1{}, (s + 1) % ST, I0{}, IH{}, s, st + ST);
+            }
         }
     }
-    if constexpr (!BVEC) fold(acc[FM - 1][FN - 1], part[kMF - 1], prev_a, nullptr);
+    if constexpr (!BVEC) fold(acc[FM - 1][FN - 1], part[kParts - 1], prev_a, nullptr);
     wait_vmcnt<0>();  // the prefetches past the end
 
     if constexpr (SPLIT) {
@@ -350,7 +543,7 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         for (int t = 0; t < kMF; ++t)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const v16f& v = acc[t % FM][t / FM];
+                const float(&v)[16] = acc[t % FM][t / FM];
                 const uint64_t pair = __float_as_uint(v[2 * q]) |
                                       (uint64_t)__float_as_uint(v[2 * q + 1]) << 32;
                 __hip_atomic_store(at(share, t) + 64 * q, pair, __ATOMIC_RELAXED,
@@ -385,7 +578,7 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
                         pair[i][q] = __hip_atomic_load(
                             at(s0 + i < p.splits ? s0 + i : s0, t) + 64 * q, __ATOMIC_RELAXED,
                             __HIP_MEMORY_SCOPE_AGENT);
-                v16f& v = acc[t % FM][t / FM];
+                float(&v)[16] = acc[t % FM][t / FM];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     if (s0 + i >= p.splits) break;
@@ -477,8 +670,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void block_gemm_split_kernel(BlockT
                                                                      smem);
 }
 
-// Tiles: kWide 128 x 256, kTall 256 x 128, kMid 128 x 128, kSmall 64 x 64.
-enum class BlockCfg { kWide, kTall, kMid, kSmall };
+// Tiles: kWide 128 x 256, kTall 256 x 128, kMid 128 x 128, kSmall 64 x 64,
+// kBig 256 x 256 (a step per tile of B).
+enum class BlockCfg { kWide, kTall, kMid, kSmall, kBig };
 // How a product of 64 x 64 tiles is split along k: 1 for not at all.
 int block_gemm_splits(int64_t m, int64_t n, int64_t k);
 hipError_t launch_block_skinny(const BlockGemmLaunch& g, hipStream_t stream);  // NT, m <= 64
@@ -537,6 +731,10 @@ hipError_t launch_block_small(const BlockGemmLaunch& g, hipStream_t stream) {
 template <int FA, int FB, bool AMN, bool BMN, bool BVEC>
 hipError_t launch_block_cfg(const BlockGemmLaunch& g, BlockCfg c, hipStream_t stream) {
     switch (c) {
+        case BlockCfg::kBig:
+            if constexpr (!BVEC)
+                return launch_block_tile<FA, FB, AMN, BMN, BVEC, 256, 256, 2, 4, 2>(g, stream);
+            else return hipErrorInvalidValue;  // (not chosen)
         case BlockCfg::kSmall: return launch_block_small<FA, FB, AMN, BMN, BVEC>(g, stream);
         case BlockCfg::kWide:
             return launch_block_tile<FA, FB, AMN, BMN, BVEC, 128, 256, 2, 4, 3>(g, stream);
