@@ -129,6 +129,8 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
         return fail(FP8_EINVAL, "%s: lda %lld < %lld", who, (long long)lda, (long long)a_cols);
     if (ldb < b_cols)
         return fail(FP8_EINVAL, "%s: ldb %lld < %lld", who, (long long)ldb, (long long)b_cols);
+    if (lda >= (1 << 24) || ldb >= (1 << 24))
+        return fail(FP8_EINVAL, "%s: lda, ldb must be below 2^24", who);
     if ((double)m * (double)n >= 1099511627776.0 ||
         (double)(trans_a ? k : m) * (double)lda >= 9.0e15 ||
         (double)(trans_b ? n : k) * (double)ldb >= 9.0e15)

@@ -19,59 +19,95 @@ namespace {
 
 // The general kernel: two LDS stages of one group of k in the tiled kernels'
 // layout.  Operands come through registers: a lane's 16 bytes may begin at
-// any address (the vector memory unit takes unaligned ones); where the
-// matrix ends inside them, the row's last 16 are loaded and shifted down.
-// Two stages are in flight in registers while one is multiplied.  Both
-// operands' steps are per line here (a tile's is repeated), and all offsets
-// are 64-bit.
-template <bool MN, int R, int NW>
+// any address (the vector memory unit takes unaligned ones).  Where the
+// matrix ends inside them, the row's last 16 are loaded instead, and shifted
+// down on their way to LDS, so that no load waits for another (SHORT: rows of
+// fewer than 16 bytes, gathered one by one).  kAhead stages are in flight in
+// registers while one is multiplied.  Both operands' steps are per line here
+// (a tile's is repeated).  Bound by the chain of a stage (LDS writes, barrier,
+// LDS reads, matrix instructions, sums): 1000 x 1111 x 2047 NN 22.6 us; three or
+// four stages ahead 23.9 / 24.1.
+template <bool MN, int R, int NW, bool SHORT>
 struct AnyOperand {
     using Op = Operand<MN, R, NW, kGroup>;
     static constexpr int kPer = Op::kPerWave;
+    static constexpr int kRowsPer = MN ? 1024 / R : 8;  // stored rows a load covers
     uint4 v[kPer];
 
-    // The stage at k0: `base` is the operand at this tile's first line.
-    __device__ void load(const uint8_t* base, int64_t ld, int64_t lines, int64_t k0, int64_t k,
-                         int wave, int lane) {
-        const int64_t rows = MN ? k : lines, width = MN ? lines : k;
+    // This lane's place in a load: stored row among its kRowsPer, first byte
+    // (the same for every load of a wave).
+    __device__ static void place(int wave, int lane, int& row, int& byte) {
+        int c;
+        Op::slot(0, wave, lane, row, c);
+        row -= kRowsPer * wave;
+        byte = 16 * c;
+    }
+    // `at`: the tile's first line at the stage's first k (uniform).  Of the
+    // stage, `lines` lines and `k` of its 128 k exist.
+    __device__ __forceinline__ void load(const uint8_t* at, int64_t ld, int lines, int k, int wave,
+                                         int lane) {
+        int row, byte;
+        place(wave, lane, row, byte);
+        const int rows = MN ? k : lines, width = MN ? lines : k;
+        if constexpr (SHORT) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            int row, c;
-            Op::slot(j, wave, lane, row, c);
-            const int64_t across = MN ? k0 + row : row;       // which stored row
-            const int64_t along = MN ? 16 * c : k0 + 16 * c;  // first byte in it
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (across >= rows || along >= width) continue;
-            const uint8_t* src = base + across * ld;
-            const int64_t over = along + 16 - width;  // bytes past the row's end
-            if (over <= 0) {
-                __builtin_memcpy(&v[j], src + along, 16);
-            } else if (width >= 16) {
-                uint64_t w[2];
-                __builtin_memcpy(w, src + width - 16, 16);
-                const int bits = 8 * (int)over;  // 8 .. 120
-                const uint64_t lo = bits < 64 ? w[0] >> bits | w[1] << (64 - bits)
-                                              : w[1] >> (bits - 64);
-                const uint64_t hi = bits < 64 ? w[1] >> bits : 0;
-                v[j] = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
-                                  (uint32_t)(hi >> 32));
-            } else {  // the whole row is shorter
+            for (int j = 0; j < kPer; ++j) {
+                const int r = kRowsPer * (wave + j * NW) + row;
                 uint64_t w[2] = {0, 0};
-                for (int i = 0; i < width; ++i)
-                    w[i / 8] |= (uint64_t)src[along + i] << (8 * (i % 8));
+                if (r < rows)
+                    for (int i = byte; i < width && i < byte + 16; ++i)
+                        w[(i - byte) / 8] |= (uint64_t)at[(int64_t)r * ld + i]
+                                             << (8 * ((i - byte) % 8));
                 v[j] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1],
                                   (uint32_t)(w[1] >> 32));
             }
+        } else {
+            // (offsets of a tile fit 32 bits: ld < 2^24)
+            const uint32_t l = (uint32_t)ld;
+            if (lines >= R && k >= kGroup) {  // uniform: all of it exists
+                const uint32_t off = row * l + byte;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    __builtin_memcpy(&v[j], at + kRowsPer * (wave + j * NW) * ld + off, 16);
+            } else {
+                // from 16 bytes before: a last piece may begin before this stage
+                const uint32_t b = 16 + (byte + 16 <= width ? byte : width - 16);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int r = kRowsPer * (wave + j * NW) + row;
+                    __builtin_memcpy(&v[j], at - 16 + ((r < rows ? r : rows - 1) * l + b), 16);
+                }
+            }
         }
     }
-    __device__ void store(uint8_t* lds, int wave, int lane) const {
+    __device__ __forceinline__ void store(uint8_t* lds, int lines, int k, int wave, int lane) {
+        const int rows = MN ? k : lines, width = MN ? lines : k;
+        const bool whole = (lines >= R && k >= kGroup) || SHORT;  // uniform
+        int row, byte;
+        place(wave, lane, row, byte);
+        if (!whole) {
+            const int over = byte + 16 - width;  // bytes past the row's end
+            const int bits = over <= 0 ? 0 : over >= 16 ? 128 : 8 * over;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const uint64_t w0 = v[j].x | (uint64_t)v[j].y << 32;
+                const uint64_t w1 = v[j].z | (uint64_t)v[j].w << 32;
+                uint64_t lo = w0, hi = w1;
+                if (bits > 0 && bits < 64) lo = w0 >> bits | w1 << (64 - bits), hi = w1 >> bits;
+                if (bits >= 64) lo = w1 >> (bits & 63), hi = 0;
+                const bool out = bits == 128 || kRowsPer * (wave + j * NW) + row >= rows;
+                v[j] = out ? make_uint4(0, 0, 0, 0)
+                           : make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi,
+                                        (uint32_t)(hi >> 32));
+            }
+        }
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             *reinterpret_cast<uint4*>(lds + 1024 * (wave + j * NW) + 16 * lane) = v[j];
     }
 };
 
-template <int FA, int FB, bool AMN, bool BMN, int BM, int BN, int WM, int WN>
+template <int FA, int FB, bool AMN, bool BMN, int BM, int BN, int WM, int WN, bool SHORT>
 __global__ __launch_bounds__(WM* WN * 64) void block_gemm_general_kernel(BlockGemmLaunch p,
                                                                         int64_t tiles,
                                                                         int64_t tiles_n) {
@@ -80,8 +116,9 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_general_kernel(BlockGe
     constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FN = TN / 32;
     static_assert(TM == 32, "one row tile per wave");
     static_assert(BM + BN <= NW * 64, "a step per lane");
-    using OA = AnyOperand<AMN, BM, NW>;
-    using OB = AnyOperand<BMN, BN, NW>;
+    using OA = AnyOperand<AMN, BM, NW, SHORT>;
+    using OB = AnyOperand<BMN, BN, NW, SHORT>;
+    constexpr int kAhead = 2;
     constexpr int kRowA = AMN ? 0 : kGroup, kRowB = BMN ? 0 : kGroup;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -111,18 +148,25 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_general_kernel(BlockGe
             OA a;
             OB b;
             float s = 0.0f;
-        } one, two;
+        } v[kAhead];
+        const int arows = p.m - m0 < BM ? (int)(p.m - m0) : BM;
+        const int brows = p.n - n0 < BN ? (int)(p.n - n0) : BN;
+        auto k_left = [&](int64_t g) {
+            const int64_t l = p.k - g * kGroup;
+            return l < kGroup ? (int)l : kGroup;
+        };
         auto load = [&](Stage& v, int64_t g) __attribute__((always_inline)) {
             if (g >= groups) return;
-            v.a.load(a, p.lda, p.m - m0, g * kGroup, p.k, wave, lane);
-            v.b.load(b, p.ldb, p.n - n0, g * kGroup, p.k, wave, lane);
+            const int64_t k0 = g * kGroup;
+            v.a.load(a + (AMN ? k0 * p.lda : k0), p.lda, arows, k_left(g), wave, lane);
+            v.b.load(b + (BMN ? k0 * p.ldb : k0), p.ldb, brows, k_left(g), wave, lane);
             if (step) v.s = step[g * step_k];
         };
-        auto store = [&](const Stage& v, int64_t g) __attribute__((always_inline)) {
+        auto store = [&](Stage& v, int64_t g) __attribute__((always_inline)) {
             if (g >= groups) return;
             uint8_t* at = smem + (g & 1) * kStage;
-            v.a.store(at, wave, lane);
-            v.b.store(at + BM * kGroup, wave, lane);
+            v.a.store(at, arows, k_left(g), wave, lane);
+            v.b.store(at + BM * kGroup, brows, k_left(g), wave, lane);
             if (e < BM + BN) *reinterpret_cast<float*>(at + (BM + BN) * kGroup + 4 * e) = v.s;
         };
         v16f acc[FN];
@@ -155,39 +199,51 @@ __global__ __launch_bounds__(WM* WN * 64) void block_gemm_general_kernel(BlockGe
                 }
             }
         };
-        // Stage g is in LDS, g + 1 in `next` and g + 2 on its way: `next` goes
-        // to the slot that stage g - 1 left before the last barrier.
-        auto turn = [&](Stage& next, int64_t g) __attribute__((always_inline)) {
-            store(next, g + 1);
-            load(next, g + 3);
-            multiply(g);
-            __syncthreads();
-        };
-        load(one, 0);
-        load(two, 1);
-        store(one, 0);
-        load(one, 2);
+        // Stage g is in LDS, the next kAhead on their way: g + 1 goes to the
+        // slot that stage g - 1 left before the last barrier.
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) load(v[x], x);
+        store(v[0], 0);
+        load(v[0], kAhead);
         __syncthreads();
-        for (int64_t g = 0; g < groups; g += 2) {
-            turn(two, g);
-            if (g + 1 < groups) turn(one, g + 1);
-        }
-        // acc[j][e] is row m0 + wm*TM + lane%32, column n0 + wn*TN + 32j +
-        // 8*(e/4) + 4*(lane/32) + e%4
-        const int64_t gm = m0 + wm * TM + (lane & 31);
-        if (gm < p.m) {
+        for (int64_t g0 = 0; g0 < groups; g0 += kAhead) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int64_t gn =
-                        n0 + wn * TN + 32 * j + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
-                    if (gn < p.n) {
-                        const float bias = p.bias ? bf16_to_f32(p.bias[gn]) : 0.0f;
-                        p.out[gm * p.n + gn] = f32_to_bf16(acc[j][i] + bias);
-                    }
-                }
+            for (int x = 0; x < kAhead; ++x) {
+                const int64_t g = g0 + x;
+                if (g >= groups) break;
+                store(v[(x + 1) % kAhead], g + 1);
+                load(v[(x + 1) % kAhead], g + 1 + kAhead);
+                multiply(g);
+                __syncthreads();
+            }
         }
+        // acc[j][e] is row wm*TM + lane%32, column wn*TN + 32j + 8*(e/4) +
+        // 4*(lane/32) + e%4 of the tile: through LDS (the operands' last use is
+        // behind a barrier), then out by whole rows
+        constexpr int kRow = BN + 4;  // bf16 per staged row
+        static_assert(BM * kRow * 2 <= 2 * kStage, "the tile fits");
+        uint16_t* out = reinterpret_cast<uint16_t*>(smem);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = wn * TN + 32 * j + 8 * q + 4 * (lane >> 5);
+                float bias[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    bias[i] = p.bias && n0 + col + i < p.n ? bf16_to_f32(p.bias[n0 + col + i])
+                                                           : 0.0f;
+                const uint2 w = make_uint2(
+                    f32x2_to_bf16x2(acc[j][4 * q] + bias[0], acc[j][4 * q + 1] + bias[1]),
+                    f32x2_to_bf16x2(acc[j][4 * q + 2] + bias[2], acc[j][4 * q + 3] + bias[3]));
+                *reinterpret_cast<uint2*>(out + (wm * TM + (lane & 31)) * kRow + col) = w;
+            }
+        __syncthreads();
+        for (int row = wave; row < BM && m0 + row < p.m; row += NW)
+#pragma unroll
+            for (int c = lane; c < BN; c += 64)
+                if (n0 + c < p.n) p.out[(m0 + row) * p.n + n0 + c] = out[row * kRow + c];
+        __syncthreads();  // before the next tile's operands
     }
 }
 
@@ -197,12 +253,15 @@ hipError_t launch_general_layout(const BlockGemmLaunch& g, hipStream_t stream) {
     auto grid = [](int64_t t) { return dim3((unsigned)(t < (1 << 20) ? t : 1 << 20)); };
     // 128 x 128 tiles read half the operand bytes per output that 64 x 64 ones
     // do, once there are enough of them for every CU.
-    if (tiles(128) >= 256)
-        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 128, 128, 4, 2>),
+    if ((AMN ? g.m : g.k) < 16 || (BMN ? g.n : g.k) < 16)
+        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 64, 64, 2, 2, true>),
+                           grid(tiles(64)), dim3(256), 0, stream, g, tiles(64), (g.n + 63) / 64);
+    else if (tiles(128) >= 256)
+        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 128, 128, 4, 2, false>),
                            grid(tiles(128)), dim3(512), 0, stream, g, tiles(128),
                            (g.n + 127) / 128);
     else
-        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 64, 64, 2, 2>),
+        hipLaunchKernelGGL((block_gemm_general_kernel<FA, FB, AMN, BMN, 64, 64, 2, 2, false>),
                            grid(tiles(64)), dim3(256), 0, stream, g, tiles(64), (g.n + 63) / 64);
     return hipGetLastError();
 }

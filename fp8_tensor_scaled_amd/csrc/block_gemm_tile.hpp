@@ -593,40 +593,49 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
     }
 
     // acc[i][j][e] is row m0 + wm*TM + 32i + lane%32, column
-    // n0 + wn*TN + 32j + 8*(e/4) + 4*(lane/32) + e%4.
-    if (p.vec_out16) {
-        // through LDS, as the per-tensor kernel: whole 16-byte chunks per row
-        constexpr int kRowBytes = TN * 2, kChunks = kRowBytes / 16;
-        constexpr int kRowsPerPass = 64 / kChunks, kRegion = TM * kRowBytes;
-        static_assert(NW * kRegion <= ST * kStage, "epilogue staging fits the ring");
-        barrier();
-        uint8_t* wl = smem + wave * kRegion;
+    // n0 + wn*TN + 32j + 8*(e/4) + 4*(lane/32) + e%4: through LDS, as the
+    // per-tensor kernel, so that the stores go by rows (in 16-byte chunks,
+    // swizzled by row, where the output's rows are whole ones).
+    constexpr int kRowBytes = TN * 2, kChunks = kRowBytes / 16;
+    constexpr int kRowsPerPass = 64 / kChunks, kRegion = TM * kRowBytes;
+    static_assert(NW * kRegion <= ST * kStage, "epilogue staging fits the ring");
+    barrier();
+    uint8_t* wl = smem + wave * kRegion;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
+    for (int j = 0; j < FN; ++j) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int cl = 32 * j + 8 * q + 4 * (lane >> 5);
-                const int64_t gn = n0 + wn * TN + cl;
-                float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (p.bias && gn < p.n) {
-                    const uint2 bb = *reinterpret_cast<const uint2*>(p.bias + gn);
-                    bias[0] = bf16_lo(bb.x); bias[1] = bf16_hi(bb.x);
-                    bias[2] = bf16_lo(bb.y); bias[3] = bf16_hi(bb.y);
-                }
+        for (int q = 0; q < 4; ++q) {
+            const int cl = 32 * j + 8 * q + 4 * (lane >> 5);
+            const int64_t gn = n0 + wn * TN + cl;
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (p.bias) {
+                if (p.vec_out16) {
+                    if (gn < p.n) {
+                        const uint2 bb = *reinterpret_cast<const uint2*>(p.bias + gn);
+                        bias[0] = bf16_lo(bb.x); bias[1] = bf16_hi(bb.x);
+                        bias[2] = bf16_lo(bb.y); bias[3] = bf16_hi(bb.y);
+                    }
+                } else {
 #pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const int row = 32 * i + (lane & 31);
-                    const int chunk = (cl >> 3) ^ (row % kChunks);
-                    v2i pk;
-                    pk[0] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 0] + bias[0],
-                                                 acc[i][j][4 * q + 1] + bias[1]);
-                    pk[1] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 2] + bias[2],
-                                                 acc[i][j][4 * q + 3] + bias[3]);
-                    *reinterpret_cast<__attribute__((address_space(3))) v2i*>(
-                        (lds_void*)(wl + row * kRowBytes + chunk * 16 + 8 * (lane >> 5))) = pk;
+                    for (int c = 0; c < 4; ++c)
+                        if (gn + c < p.n) bias[c] = bf16_to_f32(p.bias[gn + c]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int row = 32 * i + (lane & 31);
+                const int chunk = (cl >> 3) ^ (row % kChunks);
+                v2i pk;
+                pk[0] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 0] + bias[0],
+                                             acc[i][j][4 * q + 1] + bias[1]);
+                pk[1] = (int)f32x2_to_bf16x2(acc[i][j][4 * q + 2] + bias[2],
+                                             acc[i][j][4 * q + 3] + bias[3]);
+                *reinterpret_cast<__attribute__((address_space(3))) v2i*>(
+                    (lds_void*)(wl + row * kRowBytes + chunk * 16 + 8 * (lane >> 5))) = pk;
+            }
         }
+    }
+    if (p.vec_out16) {
         const int cc = lane % kChunks;
         const int64_t gn = n0 + wn * TN + 8 * cc;
 #pragma unroll
@@ -639,19 +648,17 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         }
         return;
     }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int64_t gn = n0 + wn * TN + 32 * j + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-            if (gn >= p.n) continue;
-            const float bias = p.bias ? bf16_to_f32(p.bias[gn]) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int64_t gm = m0 + wm * TM + 32 * i + (lane & 31);
-                if (gm < p.m) p.out[gm * p.n + gn] = f32_to_bf16(acc[i][j][e] + bias);
-            }
-        }
+    constexpr int kRowsPer = 64 / TN;  // one output a lane
+    static_assert(TN <= 64, "a lane per column");
+    const int col = lane % TN;
+    const int64_t gn = n0 + wn * TN + col;
+    for (int ps = 0; ps < TM / kRowsPer; ++ps) {
+        const int row = ps * kRowsPer + lane / TN;
+        const int64_t gm = m0 + wm * TM + row;
+        const uint16_t v = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(
+            (lds_void*)(wl + row * kRowBytes + (((col >> 3) ^ (row % kChunks)) << 4) +
+                        2 * (col & 7)));
+        if (gm < p.m && gn < p.n) p.out[gm * p.n + gn] = v;
     }
 }
 

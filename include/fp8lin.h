@@ -498,7 +498,8 @@ fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, i
  *   out[i][j] = bf16_rne( sum_kb sa(i,kb) sb(kb,j) sum_{k in kb} A[i][k] B[k][j] + bias[j] )
  *
  * with kb the groups of 128 k and fp32 sums.
- * a, b, trans_a, trans_b, m, n, k, lda, ldb: storage as fp8_mm (one batch).
+ * a, b, trans_a, trans_b, m, n, k, lda, ldb: storage as fp8_mm (one batch),
+ *     lda, ldb < 2^24.
  * fmt_a, fmt_b: the operands' formats, which may differ (an E5M2 gradient
  *     times an E4M3 weight).
  * group_a: FP8_GROUP_LINE -- a step for each row of A and group of k: the

@@ -83,7 +83,9 @@ def mm_args(**over):
     (dict(trans_a=1, lda=3), "lda 3 < 4"),
     (dict(trans_b=0, ldb=7), "ldb 7 < 8"),
     (dict(m=1 << 30, n=1 << 20), "too large"),
-    (dict(m=1 << 30, lda=1 << 24), "too large"),
+    (dict(m=1 << 39, n=1, lda=1 << 23), "too large"),
+    (dict(lda=1 << 24), "below 2^24"),
+    (dict(ldb=1 << 24), "below 2^24"),
     (dict(out=P(0x1001)), "aligned"),
     (dict(bias=P(0x1001)), "aligned"),
     (dict(scale_a=P(0x1002)), "aligned"),
