@@ -14,9 +14,9 @@
 //    or 64 rows of W2, for all of the expert's tokens; its 4 waves take the
 //    128-k blocks in turn, so every byte of x and of the weights is loaded by
 //    one wave of it, and the four partial sums meet in LDS in a fixed order.
-//  * Weights go straight into registers in the matrix instruction's layout
-//    (16 rows x 64 bytes per load), one block ahead, are widened to bf16
-//    (exact) and multiplied by bf16 activations: 16 tokens ride on one
+//  * Weights go straight into registers by whole lines, one block ahead, are
+//    brought into the matrix instruction's layout by lane permutes, widened to
+//    bf16 (exact) and multiplied by bf16 activations: 16 tokens ride on one
 //    16x16x32 instruction, so one token costs what 16 do.
 //  * A block of 128 k lies in one tile of steps: its four instructions start
 //    from zero, and the sum times the step is added in fp32.
@@ -62,10 +62,14 @@ struct MoeWs {
     float* logits;          // [tokens][experts]
     int32_t* ids;           // [tokens][top_k]
     float* weights;         // [tokens][top_k]
-    uint16_t* h_hi;         // bf16 [tokens * top_k][hidden]
-    uint16_t* h_lo;
+    uint16_t* h;            // bf16 [tokens * top_k][moe_h_row(hidden)]
     float* part;            // [tokens * top_k][dim], an expert's output for a token
 };
+
+// Elements of a slot's hidden activations (see moe_h_place).
+constexpr int64_t moe_h_row(int64_t hidden) {
+    return (hidden + kGroup - 1) / kGroup * (2 * kGroup);
+}
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -89,8 +93,7 @@ MoeWs layout(void* ws, int64_t t, int64_t e, int64_t k, int64_t d, int64_t h, si
     w.logits = reinterpret_cast<float*>(take(4 * t * e));
     w.ids = reinterpret_cast<int32_t*>(take(4 * t * k));
     w.weights = reinterpret_cast<float*>(take(4 * t * k));
-    w.h_hi = reinterpret_cast<uint16_t*>(take(2 * t * k * h));
-    w.h_lo = reinterpret_cast<uint16_t*>(take(2 * t * k * h));
+    w.h = reinterpret_cast<uint16_t*>(take(2 * t * k * moe_h_row(h)));
     w.part = reinterpret_cast<float*>(take(4 * t * k * d));
     *total = at;
     return w;
@@ -368,77 +371,95 @@ __device__ __forceinline__ bf16x8 as_bf16(const uint4& v) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
+typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
+
 // kTiles 16-row tiles of weights times the activations of 16 tokens over the
 // 128-k blocks wave, wave + 4, ... of `kdim`: acc[tile] += step * sum.
-// Lane l holds rows l % 16 and k = 64 i + 16 (l / 16) .. + 15 of a block (i =
-// 0, 1) on both sides, which is a reordering of k that the sum does not see.
+//
+// A load takes whole 128-byte lines of 8 rows (lane l: row l % 8, bytes 16 (l / 8)
+// ..); with loads of 16 rows x 64 bytes, as the matrix instruction has them, 64
+// tokens took 124 us instead of 109.  Each weight is read once, so with STREAM
+// past the caches (112 us without); not where kdim is no multiple of 128, since a
+// row's pieces then share lines (13 tokens, 1040 x 688: 25.3 us, 29.0 with).
+// Between a tile's two loads lanes l and l ^ 8 then exchange halves, by one lane permute
+// per register, so that lane l holds row l % 16 and k = 32 (l / 16) .. + 31 of
+// the block: a reordering of k that the sum does not see.
 //   w[tile]: the tile's first row;  s[tile]: its steps (both uniform).
-//   act[ACT]: activations, of which this lane's token's begin at element
-//   `at` (the second ones are added: what the first's rounding left).
-template <int FMT, int ACT>
+//   act, at: this lane's token's activations begin at element `at`; H: they
+//   are hidden activations, as moe_h_place lays them out.
+template <int FMT, bool H, bool STREAM>
 __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
                                               const float* const (&s)[kTiles],
-                                              const uint16_t* const (&act)[ACT], uint32_t at,
-                                              int kdim, int wave, int lane,
-                                              v4f (&acc)[kTiles]) {
-    const int kq = 16 * (lane / 16);
-    const uint32_t wo = (uint32_t)((lane % 16) * kdim + kq);
-    const uint32_t xo = 2 * (at + kq);
-    auto load16 = [](const void* base, uint32_t offset) __attribute__((always_inline)) {
-        return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + offset);
-    };
+                                              const uint16_t* act, uint32_t at, int kdim,
+                                              int wave, int lane, v4f (&acc)[kTiles]) {
+    constexpr int kParts = H ? 2 : 1;  // a hidden activation's two numbers
+    const int wk = 16 * (lane / 8), xk = 32 * (lane / 16);
+    const uint32_t wo = (uint32_t)((lane % 8) * kdim + wk);
+    const uint32_t xo = 2 * (at + (H ? 8 * (lane / 16) : xk));
     struct Block {
-        uint4 w[kTiles][2];
-        uint4 x[ACT][2][2];
+        vec4 w[kTiles][2];
+        uint4 x[kParts][4];
         float s[kTiles];
     };
     auto load = [&](int n, Block& b) __attribute__((always_inline)) {
-        const bool whole = kGroup * (n + 1) <= kdim;  // uniform
+        const int k0 = kGroup * n;
+        const bool whole = k0 + kGroup <= kdim;  // uniform
+        // kdim is a multiple of 16: a lane's 16 k of a load exist or none does
+        const uint32_t wat = wo + (whole || k0 + wk < kdim ? k0 : -wk);  // (one that exists instead)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k0 = kGroup * n + 64 * i;
-            // kdim is a multiple of 16: a lane's 16 k exist or none does
-            const bool in = whole || k0 + kq < kdim;
-            const int k = in ? k0 : -kq;  // (one that exists instead)
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) b.w[t][i] = load16(w[t], wo + k);
-#pragma unroll
-            for (int a = 0; a < ACT; ++a) {
-                b.x[a][i][0] = load16(act[a], xo + 2 * k);
-                b.x[a][i][1] = load16(act[a], xo + 2 * k + 16);
+            for (int i = 0; i < 2; ++i)
+            {
+                const vec4* src = reinterpret_cast<const vec4*>(w[t] + 8 * i * kdim + wat);
+                if constexpr (STREAM) b.w[t][i] = __builtin_nontemporal_load(src);
+                else b.w[t][i] = *src;
             }
-            if (!whole) {
-                auto keep = [&](uint4& v) __attribute__((always_inline)) {
-                    v.x = in ? v.x : 0u;
-                    v.y = in ? v.y : 0u;
-                    v.z = in ? v.z : 0u;
-                    v.w = in ? v.w : 0u;
-                };
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) keep(b.w[t][i]);
+        for (int a = 0; a < kParts; ++a)
 #pragma unroll
-                for (int a = 0; a < ACT; ++a) keep(b.x[a][i][0]), keep(b.x[a][i][1]);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t x;
+                if constexpr (H) x = xo + 4 * k0 + 256 * a + 64 * j;
+                else x = xo + (whole || k0 + xk + 8 * j < kdim ? 2 * k0 + 16 * j : -2 * xk);
+                b.x[a][j] = *reinterpret_cast<const uint4*>(
+                    reinterpret_cast<const uint8_t*>(act) + x);
             }
+        if (!whole) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (k0 + wk >= kdim) b.w[t][i] = vec4{0, 0, 0, 0};
+#pragma unroll
+            for (int a = 0; a < kParts; ++a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k0 + xk + 8 * j >= kdim) b.x[a][j] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) b.s[t] = s[t][n];
     };
-    auto multiply = [&](const Block& k) __attribute__((always_inline)) {
+    auto multiply = [&](const Block& b) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
+            vec4 f[2];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int w0 = (int)b.w[t][0][d], w1 = (int)b.w[t][1][d];
+                // row_ror:8 into lanes 8 .. 15, and into 0 .. 7, of each 16
+                f[0][d] = (uint32_t)__builtin_amdgcn_update_dpp(w0, w1, 0x128, 0xf, 0xc, false);
+                f[1][d] = (uint32_t)__builtin_amdgcn_update_dpp(w1, w0, 0x128, 0xf, 0x3, false);
+            }
             v4f part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bf16x8 lo = widen<FMT>(k.w[t][i].x, k.w[t][i].y);
-                const bf16x8 hi = widen<FMT>(k.w[t][i].z, k.w[t][i].w);
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8 m = widen<FMT>(f[j / 2][2 * (j % 2)], f[j / 2][2 * (j % 2) + 1]);
 #pragma unroll
-                for (int a = 0; a < ACT; ++a) {
-                    part = mfma_bf16(lo, as_bf16(k.x[a][i][0]), part);
-                    part = mfma_bf16(hi, as_bf16(k.x[a][i][1]), part);
-                }
+                for (int a = 0; a < kParts; ++a) part = mfma_bf16(m, as_bf16(b.x[a][j]), part);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(part[i], k.s[t], acc[t][i]);
+            for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(part[i], b.s[t], acc[t][i]);
         }
     };
     const int blocks = (kdim + kGroup - 1) / kGroup;
@@ -451,6 +472,14 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
         if (b + 2 * kWaves < blocks) load(b + 2 * kWaves, one);
         if (b + kWaves < blocks) multiply(two);
     }
+}
+
+// Hidden activations lie as the down kernel's loads take them: a row of
+// moe_h_row elements per slot, of each 128 units the rounded numbers and then
+// the rests, unit 32 q + 8 j + e of them at 32 j + 8 q + e.
+__device__ __forceinline__ int moe_h_place(int f) {
+    const int r = f % kGroup;
+    return f / kGroup * (2 * kGroup) + 32 * (r / 8 % 4) + 8 * (r / 32) + r % 8;
 }
 
 // The waves' sums of a kTiles x 16 x 16 result, added in wave order: thread
@@ -475,7 +504,7 @@ __device__ __forceinline__ void join_waves(const v4f (&acc)[kTiles], Partial& re
     __syncthreads();
 }
 
-template <int FMT>
+template <int FMT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
     if ((int)blockIdx.y >= *ws.reached_n) return;
@@ -501,21 +530,21 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
         // lanes past the list repeat its last token; their results are dropped
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
         const int slot = ws.slots[work.first + c];
-        const uint16_t* const x[1] = {p.x};
         v4f acc[kTiles] = {};
-        tile_products<FMT, 1>(w, s, x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave, lane, acc);
+        tile_products<FMT, false, STREAM>(w, s, p.x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave,
+                                  lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
-            const int64_t o = (int64_t)ws.slots[work.first + c0 + tid / 16] * p.hidden + f0 +
-                              tid % 16;
+            uint16_t* row = ws.h + ws.slots[work.first + c0 + tid / 16] * moe_h_row(p.hidden);
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
                 const float h = v[i] / (1.0f + expf(-v[i])) * v[kHalf + i];
                 const uint16_t hi = f32_to_bf16(h);
                 if (f0 + 16 * i < p.hidden) {
-                    ws.h_hi[o + 16 * i] = hi;
-                    ws.h_lo[o + 16 * i] = f32_to_bf16(h - bf16_to_f32(hi));
+                    uint16_t* at = row + moe_h_place(f0 + 16 * i + tid % 16);
+                    at[0] = hi;
+                    at[kGroup] = f32_to_bf16(h - bf16_to_f32(hi));
                 }
             }
         }
@@ -526,7 +555,7 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
 // that brings the last of the token's shares for these rows adds them up, in
 // the order of the token's choices (so the result does not depend on which
 // came last).
-template <int FMT>
+template <int FMT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
     __shared__ int done[16];  // tokens of this round that are complete, else -1
@@ -548,10 +577,9 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs w
     }
     for (int c0 = 0; c0 < work.count; c0 += 16) {
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
-        const uint32_t at = (uint32_t)(ws.slots[work.first + c] * p.hidden);
-        const uint16_t* const h[2] = {ws.h_hi, ws.h_lo};
+        const uint32_t at = (uint32_t)(ws.slots[work.first + c] * moe_h_row(p.hidden));
         v4f acc[kTiles] = {};
-        tile_products<FMT, 2>(w, s, h, at, p.hidden, wave, lane, acc);
+        tile_products<FMT, true, STREAM>(w, s, ws.h, at, p.hidden, wave, lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
@@ -624,12 +652,22 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t stream) {
     const int slots = p.tokens * p.top_k;
     const int reach = slots < p.experts ? slots : p.experts;  // at most so many experts
     const dim3 up((p.hidden + kUnits - 1) / kUnits, reach), down((p.dim + kRows - 1) / kRows, reach);
-    if (p.fmt == 0) hipLaunchKernelGGL(moe_gate_up_kernel<0>, up, dim3(kThreads), 0, stream, p, ws);
-    else hipLaunchKernelGGL(moe_gate_up_kernel<1>, up, dim3(kThreads), 0, stream, p, ws);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (p.fmt == 0) hipLaunchKernelGGL(moe_down_kernel<0>, down, dim3(kThreads), 0, stream, p, ws);
-    else hipLaunchKernelGGL(moe_down_kernel<1>, down, dim3(kThreads), 0, stream, p, ws);
-    return hipGetLastError();
+    auto launch = [&](auto fmt) {
+        constexpr int F = decltype(fmt)::value;
+        if (p.dim % kGroup == 0)
+            hipLaunchKernelGGL((moe_gate_up_kernel<F, true>), up, dim3(kThreads), 0, stream, p, ws);
+        else
+            hipLaunchKernelGGL((moe_gate_up_kernel<F, false>), up, dim3(kThreads), 0, stream, p, ws);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        if (p.hidden % kGroup == 0)
+            hipLaunchKernelGGL((moe_down_kernel<F, true>), down, dim3(kThreads), 0, stream, p, ws);
+        else
+            hipLaunchKernelGGL((moe_down_kernel<F, false>), down, dim3(kThreads), 0, stream, p, ws);
+        return hipGetLastError();
+    };
+    return p.fmt == 0 ? launch(std::integral_constant<int, 0>{})
+                      : launch(std::integral_constant<int, 1>{});
 }
 
 }  // namespace fp8lin
