@@ -14,7 +14,7 @@
 //    or 64 rows of W2, for all of the expert's tokens; its 4 waves take the
 //    128-k blocks in turn, so every byte of x and of the weights is loaded by
 //    one wave of it, and the four partial sums meet in LDS in a fixed order.
-//  * Weights go straight into registers by whole lines, one block ahead, are
+//  * Weights go straight into registers by whole lines, are
 //    brought into the matrix instruction's layout by lane permutes, widened to
 //    bf16 (exact) and multiplied by bf16 activations: 16 tokens ride on one
 //    16x16x32 instruction, so one token costs what 16 do.
@@ -39,7 +39,13 @@ constexpr int kMaxExperts = 512, kMaxTokens = 1024;
 constexpr int kRouteTokens = 4;   // tokens of a routing workgroup
 constexpr int kTiles = 4;         // 16-row tiles of weights per wave
 constexpr int kUnits = 8 * kTiles;        // hidden units of a gate / up workgroup
-constexpr int kRows = 16 * kTiles;         // rows of W2 of a down workgroup
+constexpr int kRows = 16 * kTiles;        // rows of W2 of a down workgroup
+// From this many workgroups of a product on, a wave loads a block when it has
+// used the one before, and its registers leave room for twice the waves on a
+// CU; below it a wave loads one block ahead of the one that it multiplies.
+// 64 experts of 2048 x 1024, 8 a token, whole layer: 64 tokens (2048
+// workgroups) 100 us, 108 with one ahead; 1 token (256) 26.5 us, 25.7.
+constexpr unsigned kManyGroups = 1024;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -386,8 +392,9 @@ typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
 // the block: a reordering of k that the sum does not see.
 //   w[tile]: the tile's first row;  s[tile]: its steps (both uniform).
 //   act, at: this lane's token's activations begin at element `at`; H: they
-//   are hidden activations, as moe_h_place lays them out.
-template <int FMT, bool H, bool STREAM>
+//   are hidden activations, as moe_h_place lays them out.  AHEAD: one block's
+//   loads go out before the block before it is multiplied (see kManyGroups).
+template <int FMT, bool H, bool STREAM, bool AHEAD>
 __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
                                               const float* const (&s)[kTiles],
                                               const uint16_t* act, uint32_t at, int kdim,
@@ -409,8 +416,7 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-            {
+            for (int i = 0; i < 2; ++i) {
                 const vec4* src = reinterpret_cast<const vec4*>(w[t] + 8 * i * kdim + wat);
                 if constexpr (STREAM) b.w[t][i] = __builtin_nontemporal_load(src);
                 else b.w[t][i] = *src;
@@ -463,6 +469,14 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
         }
     };
     const int blocks = (kdim + kGroup - 1) / kGroup;
+    if constexpr (!AHEAD) {
+        for (int b = wave; b < blocks; b += kWaves) {
+            Block k;
+            load(b, k);
+            multiply(k);
+        }
+        return;
+    }
     if (wave >= blocks) return;
     Block one, two;
     load(wave, one);
@@ -504,7 +518,7 @@ __device__ __forceinline__ void join_waves(const v4f (&acc)[kTiles], Partial& re
     __syncthreads();
 }
 
-template <int FMT, bool STREAM>
+template <int FMT, bool STREAM, bool AHEAD>
 __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
     if ((int)blockIdx.y >= *ws.reached_n) return;
@@ -531,7 +545,7 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
         const int slot = ws.slots[work.first + c];
         v4f acc[kTiles] = {};
-        tile_products<FMT, false, STREAM>(w, s, p.x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave,
+        tile_products<FMT, false, STREAM, AHEAD>(w, s, p.x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave,
                                   lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
@@ -555,7 +569,7 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
 // that brings the last of the token's shares for these rows adds them up, in
 // the order of the token's choices (so the result does not depend on which
 // came last).
-template <int FMT, bool STREAM>
+template <int FMT, bool STREAM, bool AHEAD>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
     __shared__ int done[16];  // tokens of this round that are complete, else -1
@@ -579,7 +593,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs w
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
         const uint32_t at = (uint32_t)(ws.slots[work.first + c] * moe_h_row(p.hidden));
         v4f acc[kTiles] = {};
-        tile_products<FMT, true, STREAM>(w, s, ws.h, at, p.hidden, wave, lane, acc);
+        tile_products<FMT, true, STREAM, AHEAD>(w, s, ws.h, at, p.hidden, wave, lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
@@ -652,19 +666,30 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t stream) {
     const int slots = p.tokens * p.top_k;
     const int reach = slots < p.experts ? slots : p.experts;  // at most so many experts
     const dim3 up((p.hidden + kUnits - 1) / kUnits, reach), down((p.dim + kRows - 1) / kRows, reach);
-    auto launch = [&](auto fmt) {
-        constexpr int F = decltype(fmt)::value;
-        if (p.dim % kGroup == 0)
-            hipLaunchKernelGGL((moe_gate_up_kernel<F, true>), up, dim3(kThreads), 0, stream, p, ws);
-        else
-            hipLaunchKernelGGL((moe_gate_up_kernel<F, false>), up, dim3(kThreads), 0, stream, p, ws);
-        const hipError_t err = hipGetLastError();
-        if (err != hipSuccess) return err;
-        if (p.hidden % kGroup == 0)
-            hipLaunchKernelGGL((moe_down_kernel<F, true>), down, dim3(kThreads), 0, stream, p, ws);
-        else
-            hipLaunchKernelGGL((moe_down_kernel<F, false>), down, dim3(kThreads), 0, stream, p, ws);
+    using std::bool_constant;
+    auto gate_up = [&](auto fmt, auto stream_c, auto ahead) {
+        hipLaunchKernelGGL((moe_gate_up_kernel<decltype(fmt)::value, decltype(stream_c)::value,
+                                               decltype(ahead)::value>),
+                           up, dim3(kThreads), 0, stream, p, ws);
         return hipGetLastError();
+    };
+    auto down_all = [&](auto fmt, auto stream_c, auto ahead) {
+        hipLaunchKernelGGL((moe_down_kernel<decltype(fmt)::value, decltype(stream_c)::value,
+                                            decltype(ahead)::value>),
+                           down, dim3(kThreads), 0, stream, p, ws);
+        return hipGetLastError();
+    };
+    auto pick = [&](auto launch_one, auto fmt, int kdim, dim3 grid) {
+        const bool ahead = grid.x * grid.y < kManyGroups;
+        if (kdim % kGroup == 0)
+            return ahead ? launch_one(fmt, bool_constant<true>{}, bool_constant<true>{})
+                         : launch_one(fmt, bool_constant<true>{}, bool_constant<false>{});
+        return ahead ? launch_one(fmt, bool_constant<false>{}, bool_constant<true>{})
+                     : launch_one(fmt, bool_constant<false>{}, bool_constant<false>{});
+    };
+    auto launch = [&](auto fmt) {
+        const hipError_t err = pick(gate_up, fmt, p.dim, up);
+        return err == hipSuccess ? pick(down_all, fmt, p.hidden, down) : err;
     };
     return p.fmt == 0 ? launch(std::integral_constant<int, 0>{})
                       : launch(std::integral_constant<int, 1>{});
