@@ -319,8 +319,11 @@ static bool tiled_supported(const BlockGemmLaunch& g) {
 }
 
 // A backward's products go in one launch of 128 x 128 tiles up to this many of
-// them (four rounds of the CUs); beyond, each gains more from larger tiles.
-constexpr int kPairTiles = 1024;
+// them (two rounds of the CUs); beyond, each gains more from larger tiles.  Whole
+// backward, us, one launch / each its own: 512^3 (32 tiles) 11.7 / 16.8, 2048^3
+// (512) 38.8 / 43.5, 2048 x 2816 x 2048 (608) 54.3 / 53.7, 4096 x 2048 x 2048 (768)
+// 62.5 / 62.5, 4096 x 4096 x 2048 (1024) 113 / 101, 4096^3 (2048) 205 / 169.
+constexpr int kPairTiles = 512;
 
 // Below this many 128 x 128 tiles, 64 x 64 ones, which spread over more CUs
 // (us, 64 x 64 / 128 x 128: 1024^3 NT, 64 tiles of 128 x 128, 5.7 / 8.0;

@@ -344,14 +344,18 @@ BlockQuantParams params_of(const BlockQuantLaunch& q) {
     return p;
 }
 
-// 1024 lanes a tile below this many tiles, 256 from it on.
+// Below this many tiles a tile has 1024 lanes, from it on 256; rows alone, which
+// need no 128-row span, have 256 lanes per 16 rows of a tile below it.  bf16, us,
+// the first way / 256 lanes a tile: both ways 256 x 256 (4 tiles) 4.2 / 4.8, 2048 x
+// 2048 (256) 6.9 / 7.7, 2048 x 4096 (512) 10.2 / 10.7, 4096 x 4096 (1024) 17.8 / 14.3;
+// tiles 3.0 / 3.3, 4.5 / 4.9, 6.8 / 7.2, 11.2 / 10.7, 8192 x 8192 37.2 / 35.1; rows
+// 2.4 / 3.4, 4.9 / 5.3, 8.3 / 8.0, 13.1 / 11.7.
 constexpr int64_t kManyTiles = 512;
 
 template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM>
 hipError_t launch_kinds(const BlockQuantParams& p, hipStream_t stream) {
     const int64_t tiles = groups_of(p.rows) * p.col_groups;
     if constexpr (ROW && !COL && !SUM) {
-        // rows alone need no 128-row span: 16 rows a workgroup, until 128 fill the chip
         if (tiles < kManyTiles)
             hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, true, false, false, false, 256, 1>),
                                dim3((unsigned)((p.rows + 15) / 16 * p.col_groups)), dim3(256), 0,
