@@ -417,6 +417,46 @@ def test_layer_partial_gradients_and_shapes(f, ac):
     assert torch.equal(xt.grad.reshape(x.shape), full["x"])
 
 
+@pytest.mark.parametrize("M,N,K", [(2048, 2816, 2064), (2048, 2056, 2048)])
+def test_layer_backward_beyond_one_launch(f, M, N, K):
+    """Too many tiles for one launch of both products, and sides that the
+    tiled kernels do not take: the bits of the products called one by one."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+    x, w, dy = r(M, K), r(N, K), r(M, N)
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    saved = u8(f.fp8_linear_block_saved(M, N, K, True, True))
+    y, dx, dw = (torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+                 for s in ((M, N), (M, K), (N, K)))
+    db = torch.empty(N, dtype=torch.bfloat16, device="cuda")
+    zeros = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    f.fp8_linear_block_fwd(x, w, None, M, N, K, E4M3, 0, saved, True, True,
+                           zeros(f.fp8_linear_block_fwd_workspace(M, N, K)), y)
+    f.fp8_linear_block_bwd(dy, saved, M, N, K, E4M3, E5M2, 0, True, True,
+                           zeros(f.fp8_linear_block_bwd_workspace(M, N, K)), dx, dw, db)
+    G = ref.groups
+    step = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    xr, xc, sxr, sxc = u8(M, K), u8(M, K), step(M, G(K)), step(G(M), K)
+    gr, gc, sgr, sgc = u8(M, N), u8(M, N), step(M, G(N)), step(G(M), N)
+    wt, sw = u8(N, K), step(G(N), G(K))
+    f.fp8_quantize_block(x, M, K, E4M3, out_row=xr, scale_row=sxr, out_col=xc, scale_col=sxc)
+    f.fp8_quantize_block(dy, M, N, E5M2, out_row=gr, scale_row=sgr, out_col=gc, scale_col=sgc)
+    f.fp8_quantize_block(w, N, K, E4M3, out_tile=wt, scale_tile=sw)
+    y1, dx1, dw1 = (torch.empty_like(t) for t in (y, dx, dw))
+    f.fp8_mm_block(xr, wt, E4M3, E4M3, 0, 1, M, N, K, K, K, sxr, f.GROUP_LINE, sw, f.GROUP_TILE,
+                   None, y1)
+    f.fp8_mm_block(gr, wt, E5M2, E4M3, 0, 0, M, K, N, N, K, sgr, f.GROUP_LINE, sw, f.GROUP_TILE,
+                   None, dx1)
+    f.fp8_mm_block(gc, xc, E5M2, E4M3, 1, 0, N, K, M, N, K, sgc, f.GROUP_LINE, sxc, f.GROUP_LINE,
+                   None, dw1)
+    torch.cuda.synchronize()
+    for a, b in ((y, y1), (dx, dx1), (dw, dw1)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    want = host(dy).astype(np.float64).sum(0)
+    mag = np.abs(host(dy)).astype(np.float64).sum(0)
+    ref.check_close(from_dev_bf16(db.view(torch.int16)), want, M * 2.0 ** -24 * mag, "db")
+
+
 def test_layer_no_rows(f, ac):
     x = torch.empty(0, 144, device="cuda", dtype=torch.bfloat16, requires_grad=True)
     w = torch.randn(96, 144, device="cuda", dtype=torch.bfloat16, requires_grad=True)
