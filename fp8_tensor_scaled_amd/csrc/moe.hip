@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kMaxExperts = 512, kMaxTokens = 1024;
+constexpr int kMaxExperts = 512, kMaxTokens = 1024, kMaxTopK = 16;
 constexpr int kRouteTokens = 4;   // tokens of a routing workgroup
 constexpr int kTiles = 4;         // 16-row tiles of weights per wave
 constexpr int kUnits = 8 * kTiles;        // hidden units of a gate / up workgroup
@@ -169,7 +169,7 @@ __device__ __forceinline__ float reduce_sum(float v) {
 // that holds the maximum, at its first place, is the lowest index.
 template <int PER>
 __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& ws, int64_t t,
-                                               float (&v)[PER], int lane) {
+                                               float (&v)[PER], int lane, uint16_t* ids) {
     float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mx = fmaxf(mx, v[i]);
@@ -189,7 +189,7 @@ __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& 
         if (nan[i]) v[i] = taken;
         if (lane * PER + i < p.experts) left |= 1u << i;
     }
-    float chosen = 0.0f, total = 0.0f;
+    float chosen = -INFINITY;  // lane j's: the j-th expert's logit, and its index
     int chosen_id = 0;
     for (int j = 0; j < p.top_k; ++j) {
         float best = -INFINITY;
@@ -208,13 +208,13 @@ __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& 
         const int id = __builtin_amdgcn_readlane(lane * PER + at, winner);
         value = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), winner));
         if (mine) left &= ~(1u << at);
-        const float w = expf(value - mx) / sum;
-        total += w;
-        if (lane == j) chosen = w, chosen_id = id;
+        if (lane == j) chosen = value, chosen_id = id;
     }
+    float w = lane < p.top_k ? expf(chosen - mx) / sum : 0.0f;
+    if (p.renorm) w /= reduce_sum(w);
     if (lane < p.top_k) {
-        const float w = p.renorm ? chosen / total : chosen;
         const int64_t o = t * p.top_k + lane;
+        ids[lane] = (uint16_t)chosen_id;
         store_dev(ws.ids + o, chosen_id);
         ws.weights[o] = w;
         if (p.ids) p.ids[o] = chosen_id;
@@ -224,27 +224,33 @@ __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& 
 
 template <int PER>
 __device__ __forceinline__ void load_and_select(const MoeLaunch& p, const MoeWs& ws, int64_t t,
-                                                int lane) {
+                                                int lane, uint16_t* ids) {
     float v[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane * PER + i;
         v[i] = e < p.experts ? load_dev(ws.logits + t * p.experts + e) : -INFINITY;
     }
-    select_experts<PER>(p, ws, t, v, lane);
+    select_experts<PER>(p, ws, t, v, lane, ids);
 }
 
-// The list of reached experts and their slots, by one workgroup.
+// The list of reached experts and their slots, by one workgroup.  ids: every
+// slot's expert, here already if `have`.
 struct Lists {
+    uint16_t ids[kMaxTokens * kMaxTopK];
     int count[kMaxExperts], first[kMaxExperts];
     int sums[2][kWaves];
 };
-__device__ __forceinline__ void build_lists(const MoeLaunch& p, const MoeWs& ws, Lists& s) {
+__device__ __forceinline__ void build_lists(const MoeLaunch& p, const MoeWs& ws, Lists& s,
+                                            bool have) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int n = p.tokens * p.top_k;
     for (int e = tid; e < kMaxExperts; e += kThreads) s.count[e] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) atomicAdd(&s.count[load_dev(ws.ids + i)], 1);
+    for (int i = tid; i < n; i += kThreads) {
+        if (!have) s.ids[i] = (uint16_t)load_dev(ws.ids + i);
+        atomicAdd(&s.count[s.ids[i]], 1);
+    }
     __syncthreads();
     // each thread takes two neighbouring experts: slots and reached ones before them
     static_assert(kMaxExperts == 2 * kThreads, "two experts per thread");
@@ -271,7 +277,7 @@ __device__ __forceinline__ void build_lists(const MoeLaunch& p, const MoeWs& ws,
     if (tid == 0) *ws.reached_n = all;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads)
-        ws.slots[atomicAdd(&s.first[load_dev(ws.ids + i)], 1)] = i;
+        ws.slots[atomicAdd(&s.first[s.ids[i]], 1)] = i;
 }
 
 // A workgroup computes the logits of 4 experts (one a wave) for 4 tokens;
@@ -333,18 +339,16 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs 
     }
     if (!last_of(ws.route_count + blockIdx.y, gridDim.x, &flag)) return;
     const int t = t0 + wave;
+    uint16_t* ids = lists.ids + wave * p.top_k;
     if (t < p.tokens) {
-        if (p.experts <= kWave) load_and_select<1>(p, ws, t, lane);
-        else if (p.experts <= 2 * kWave) load_and_select<2>(p, ws, t, lane);
-        else load_and_select<8>(p, ws, t, lane);
+        if (p.experts <= kWave) load_and_select<1>(p, ws, t, lane, ids);
+        else if (p.experts <= 2 * kWave) load_and_select<2>(p, ws, t, lane, ids);
+        else load_and_select<8>(p, ws, t, lane, ids);
     }
-    if (gridDim.y == 1) {  // this workgroup chose for every token
-        stores_done();
-        __syncthreads();
-    } else if (!last_of(ws.group_count, gridDim.y, &flag)) {
-        return;
-    }
-    build_lists(p, ws, lists);
+    const bool all = gridDim.y == 1;  // this workgroup chose for every token
+    if (all) __syncthreads();
+    else if (!last_of(ws.group_count, gridDim.y, &flag)) return;
+    build_lists(p, ws, lists, all);
 }
 
 // Eight fp8 codes -> bf16 (exact).
