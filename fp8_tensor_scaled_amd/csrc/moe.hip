@@ -9,15 +9,16 @@
 //
 //  * The routing launch leaves a list of the experts that were reached and
 //    of each one's tokens, so that a workgroup of the products knows its work
-//    from one short read.
+//    from one short read.  One token has a form of its own, whose workgroups
+//    choose for themselves and add up the choices' shares in LDS.
 //  * A workgroup takes 32 hidden units of one expert (32 rows of G and of U)
 //    or 64 rows of W2, for all of the expert's tokens; its 4 waves take the
 //    128-k blocks in turn, so every byte of x and of the weights is loaded by
 //    one wave of it, and the four partial sums meet in LDS in a fixed order.
-//  * Weights go straight into registers by whole lines, are
-//    brought into the matrix instruction's layout by lane permutes, widened to
-//    bf16 (exact) and multiplied by bf16 activations: 16 tokens ride on one
-//    16x16x32 instruction, so one token costs what 16 do.
+//  * Weights go straight into registers by whole lines, are brought into the
+//    matrix instruction's layout by lane permutes, widened to bf16
+//    (exact) and multiplied by bf16 activations: 16 tokens ride on one 16x16x32
+//    instruction, so one token costs what 16 do.
 //  * A block of 128 k lies in one tile of steps: its four instructions start
 //    from zero, and the sum times the step is added in fp32.
 //  * The hidden activations go between the two kernels as two bf16 numbers
@@ -44,8 +45,13 @@ constexpr int kRows = 16 * kTiles;        // rows of W2 of a down workgroup
 // used the one before, and its registers leave room for twice the waves on a
 // CU; below it a wave loads one block ahead of the one that it multiplies.
 // 64 experts of 2048 x 1024, 8 a token, whole layer: 64 tokens (2048
-// workgroups) 100 us, 108 with one ahead; 1 token (256) 26.5 us, 25.7.
+// workgroups) 100 us, 108 with one ahead; one token (256 workgroups; before it
+// had its own form) 26.5 us, 25.7.
 constexpr unsigned kManyGroups = 1024;
+
+// One token: waves and outputs of a down workgroup (16 outputs a workgroup: 64
+// experts of 2048 x 1024, 8 a token, 23.3 us instead of 22.4).
+constexpr int kOneWaves = 8, kOneRows = 8;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -167,9 +173,12 @@ __device__ __forceinline__ float reduce_sum(float v) {
 // Top-k of one token by one wave.  Lane l has the logits of experts
 // l * PER .. l * PER + PER - 1 (v[], -inf past the last), so the lowest lane
 // that holds the maximum, at its first place, is the lowest index.
+struct Choice {
+    int id;
+    float w;
+};
 template <int PER>
-__device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& ws, int64_t t,
-                                               float (&v)[PER], int lane, uint16_t* ids) {
+__device__ __forceinline__ Choice select_experts(const MoeLaunch& p, float (&v)[PER], int lane) {
     float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mx = fmaxf(mx, v[i]);
@@ -212,26 +221,35 @@ __device__ __forceinline__ void select_experts(const MoeLaunch& p, const MoeWs& 
     }
     float w = lane < p.top_k ? expf(chosen - mx) / sum : 0.0f;
     if (p.renorm) w /= reduce_sum(w);
-    if (lane < p.top_k) {
-        const int64_t o = t * p.top_k + lane;
-        ids[lane] = (uint16_t)chosen_id;
-        store_dev(ws.ids + o, chosen_id);
-        ws.weights[o] = w;
-        if (p.ids) p.ids[o] = chosen_id;
-        if (p.weights) p.weights[o] = w;
-    }
+    return Choice{chosen_id, w};
 }
 
-template <int PER>
-__device__ __forceinline__ void load_and_select(const MoeLaunch& p, const MoeWs& ws, int64_t t,
-                                                int lane, uint16_t* ids) {
-    float v[PER];
+// Lane j < top_k: the j-th choice of token t.
+__device__ __forceinline__ Choice choose(const MoeLaunch& p, const MoeWs& ws, int64_t t,
+                                         int lane) {
+    auto go = [&](auto per) __attribute__((always_inline)) {
+        constexpr int kPer = decltype(per)::value;
+        float v[kPer];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane * PER + i;
-        v[i] = e < p.experts ? load_dev(ws.logits + t * p.experts + e) : -INFINITY;
-    }
-    select_experts<PER>(p, ws, t, v, lane, ids);
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane * kPer + i;
+            v[i] = e < p.experts ? load_dev(ws.logits + t * p.experts + e) : -INFINITY;
+        }
+        return select_experts<kPer>(p, v, lane);
+    };
+    using std::integral_constant;
+    if (p.experts <= kWave) return go(integral_constant<int, 1>{});
+    if (p.experts <= 2 * kWave) return go(integral_constant<int, 2>{});
+    return go(integral_constant<int, 8>{});
+}
+__device__ __forceinline__ void store_choice(const MoeLaunch& p, const MoeWs& ws, int64_t t,
+                                             int lane, Choice c) {
+    if (lane >= p.top_k) return;
+    const int64_t o = t * p.top_k + lane;
+    store_dev(ws.ids + o, c.id);
+    ws.weights[o] = c.w;
+    if (p.ids) p.ids[o] = c.id;
+    if (p.weights) p.weights[o] = c.w;
 }
 
 // The list of reached experts and their slots, by one workgroup.  ids: every
@@ -337,13 +355,13 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeLaunch p, MoeWs 
                 store_dev(ws.logits + (int64_t)(t0 + i) * p.experts + e, s);
         }
     }
+    if (p.tokens == 1) return;  // the next launch's workgroups choose
     if (!last_of(ws.route_count + blockIdx.y, gridDim.x, &flag)) return;
     const int t = t0 + wave;
-    uint16_t* ids = lists.ids + wave * p.top_k;
     if (t < p.tokens) {
-        if (p.experts <= kWave) load_and_select<1>(p, ws, t, lane, ids);
-        else if (p.experts <= 2 * kWave) load_and_select<2>(p, ws, t, lane, ids);
-        else load_and_select<8>(p, ws, t, lane, ids);
+        const Choice c = choose(p, ws, t, lane);
+        if (lane < p.top_k) lists.ids[wave * p.top_k + lane] = (uint16_t)c.id;
+        store_choice(p, ws, t, lane, c);
     }
     const bool all = gridDim.y == 1;  // this workgroup chose for every token
     if (all) __syncthreads();
@@ -383,6 +401,20 @@ __device__ __forceinline__ bf16x8 as_bf16(const uint4& v) {
 
 typedef uint32_t vec4 __attribute__((ext_vector_type(4)));
 
+// Four fp8 codes -> fp32 (exact).
+template <int FMT>
+__device__ __forceinline__ void fp8_to_f32(uint32_t w, float (&f)[4]) {
+    if constexpr (FMT) {
+        const auto a = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false);
+        const auto b = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, true);
+        f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1];
+    } else {
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+        const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+        f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1];
+    }
+}
+
 // kTiles 16-row tiles of weights times the activations of 16 tokens over the
 // 128-k blocks wave, wave + 4, ... of `kdim`: acc[tile] += step * sum.
 //
@@ -416,7 +448,8 @@ __device__ __forceinline__ void tile_products(const uint8_t* const (&w)[kTiles],
         const int k0 = kGroup * n;
         const bool whole = k0 + kGroup <= kdim;  // uniform
         // kdim is a multiple of 16: a lane's 16 k of a load exist or none does
-        const uint32_t wat = wo + (whole || k0 + wk < kdim ? k0 : -wk);  // (one that exists instead)
+        // (one that exists instead)
+        const uint32_t wat = wo + (whole || k0 + wk < kdim ? k0 : -wk);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -522,14 +555,25 @@ __device__ __forceinline__ void join_waves(const v4f (&acc)[kTiles], Partial& re
     __syncthreads();
 }
 
-template <int FMT, bool STREAM, bool AHEAD>
+// ONE: there is one token, whose top_k choices each workgroup makes for itself
+// from the logits that the launch before left, and takes the blockIdx.y-th.
+// That is cheaper than choosing before, in the last workgroup to bring its
+// logits: two round trips through memory and the lists.
+template <int FMT, bool STREAM, bool AHEAD, bool ONE>
 __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeWs ws) {
     __shared__ Partial red;
-    if ((int)blockIdx.y >= *ws.reached_n) return;
-    const Reached work = ws.reached[blockIdx.y];
-    const int64_t e = work.expert;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    Reached work;
+    if constexpr (ONE) {
+        const Choice c = choose(p, ws, 0, lane);
+        work = Reached{__builtin_amdgcn_readlane(c.id, blockIdx.y), (int)blockIdx.y, 1, 0};
+        if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) store_choice(p, ws, 0, lane, c);
+    } else {
+        if ((int)blockIdx.y >= *ws.reached_n) return;
+        work = ws.reached[blockIdx.y];
+    }
+    const int64_t e = work.expert;
     const int f0 = blockIdx.x * kUnits;
     const int kg = (p.dim + kGroup - 1) / kGroup, rg = (2 * p.hidden + kGroup - 1) / kGroup;
     constexpr int kHalf = kTiles / 2;  // tiles of gate rows, then as many of up rows
@@ -547,14 +591,15 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
     for (int c0 = 0; c0 < work.count; c0 += 16) {
         // lanes past the list repeat its last token; their results are dropped
         const int c = c0 + lane % 16 < work.count ? c0 + lane % 16 : work.count - 1;
-        const int slot = ws.slots[work.first + c];
+        const int slot = ONE ? work.first : ws.slots[work.first + c];
         v4f acc[kTiles] = {};
-        tile_products<FMT, false, STREAM, AHEAD>(w, s, p.x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave,
-                                  lane, acc);
+        tile_products<FMT, false, STREAM, AHEAD>(
+            w, s, p.x, (uint32_t)(slot / p.top_k * p.dim), p.dim, wave, lane, acc);
         float v[kTiles];
         join_waves(acc, red, v);
         if (c0 + tid / 16 < work.count) {
-            uint16_t* row = ws.h + ws.slots[work.first + c0 + tid / 16] * moe_h_row(p.hidden);
+            const int at_slot = ONE ? work.first : ws.slots[work.first + c0 + tid / 16];
+            uint16_t* row = ws.h + at_slot * moe_h_row(p.hidden);
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
                 const float h = v[i] / (1.0f + expf(-v[i])) * v[kHalf + i];
@@ -650,6 +695,97 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLaunch p, MoeWs w
     }
 }
 
+// One token: a workgroup owns kOneRows outputs, a wave of it one choice (or,
+// where there are few, a share of its blocks) at a time, so the shares meet in
+// LDS and not in memory.  Lane l has 16 k from 16 (l % 8) on of row l / 8 of each
+// block of 128, whose sum times the step is added in fp32; the matrix unit has nothing to share between tokens here.
+template <int FMT>
+__global__ __launch_bounds__(kOneWaves * kWave) void moe_down_one_kernel(MoeLaunch p, MoeWs ws) {
+    static_assert(kOneRows == kWave / 8, "8 lanes a row");
+    __shared__ float red[kMaxTopK][kOneRows];
+    const int tid = threadIdx.x, lane = tid % kWave, c = lane % 8, r = lane / 8;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int d0 = blockIdx.x * kOneRows;
+    const int kg = (p.hidden + kGroup - 1) / kGroup, rg = (p.dim + kGroup - 1) / kGroup;
+    // a choice's blocks go to several waves when there are few choices
+    const int parts = p.top_k < kOneWaves ? kOneWaves / p.top_k : 1;
+    for (int task = wave; task < p.top_k * parts; task += kOneWaves) {
+        const int j = task / parts, part_of = task % parts;
+        const int first = kg * part_of / parts, last = kg * (part_of + 1) / parts;
+        const int64_t e = ws.ids[j];
+        const uint8_t* w = p.w2 + (e * p.dim + d0) * p.hidden + (r * p.hidden + 16 * c);
+        const float* s = p.s2 + (e * rg + d0 / kGroup) * kg;
+        // (moe_h_place of the lane's first unit in a block)
+        const uint16_t* h = ws.h + j * moe_h_row(p.hidden) + 64 * (c % 2) + 8 * (c / 2);
+        float acc = 0.0f;
+        constexpr int kBlocks = 2;  // in flight (one or three: 1.5 us more)
+        for (int b0 = first; b0 < last; b0 += kBlocks) {
+            vec4 wv[kBlocks];
+            uint4 hv[kBlocks][4];
+            float step[kBlocks];
+            bool ok[kBlocks];
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                // all of the lane's 16 k exist, or none (something that exists instead)
+                ok[i] = b0 + i < last && kGroup * (b0 + i) + 16 * c < p.hidden;
+                const int b = b0 + i < last ? b0 + i : 0;
+                wv[i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const vec4*>(w + (ok[i] ? kGroup * (b0 + i) : -16 * c)));
+#pragma unroll
+                for (int q = 0; q < 4; ++q)  // numbers, and from 128 on their rests
+                    hv[i][q] = *reinterpret_cast<const uint4*>(h + 2 * kGroup * b +
+                                                               kGroup * (q / 2) + 32 * (q % 2));
+                step[i] = s[b];
+            }
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                float part = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {  // 8 k
+                    const uint32_t hi[4] = {hv[i][q].x, hv[i][q].y, hv[i][q].z, hv[i][q].w};
+                    const uint32_t lo[4] = {hv[i][2 + q].x, hv[i][2 + q].y, hv[i][2 + q].z,
+                                            hv[i][2 + q].w};
+                    float hf[8];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        hf[2 * x] = bf16_lo(hi[x]) + bf16_lo(lo[x]);
+                        hf[2 * x + 1] = bf16_hi(hi[x]) + bf16_hi(lo[x]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float f[4];
+                        fp8_to_f32<FMT>(wv[i][2 * q + x], f);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) part = fmaf(f[z], hf[4 * x + z], part);
+                    }
+                }
+                // (kept out of a branch, into which its loads would go too)
+                float sum = fmaf(part, step[i], acc);
+                asm volatile("" : "+v"(sum));
+                acc = ok[i] ? sum : acc;
+            }
+        }
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) acc += __shfl_xor(acc, off, kWave);
+        if (c == 0) red[task][r] = acc;
+    }
+    __syncthreads();
+    if (tid < kOneRows / 2) {
+        float y0 = 0.0f, y1 = 0.0f;
+        for (int j = 0; j < p.top_k; ++j) {
+            const float g = ws.weights[j];
+            float s0 = 0.0f, s1 = 0.0f;
+            for (int i = j * parts; i < (j + 1) * parts; ++i) {
+                s0 += red[i][2 * tid];
+                s1 += red[i][2 * tid + 1];
+            }
+            y0 = fmaf(g, s0, y0);
+            y1 = fmaf(g, s1, y1);
+        }
+        *reinterpret_cast<uint32_t*>(p.out + d0 + 2 * tid) = f32x2_to_bf16x2(y0, y1);
+    }
+}
+
 }  // namespace
 
 size_t moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t dim, int64_t hidden) {
@@ -669,11 +805,12 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const int slots = p.tokens * p.top_k;
     const int reach = slots < p.experts ? slots : p.experts;  // at most so many experts
-    const dim3 up((p.hidden + kUnits - 1) / kUnits, reach), down((p.dim + kRows - 1) / kRows, reach);
+    const dim3 up((p.hidden + kUnits - 1) / kUnits, reach);
+    const dim3 down((p.dim + kRows - 1) / kRows, reach);
     using std::bool_constant;
     auto gate_up = [&](auto fmt, auto stream_c, auto ahead) {
         hipLaunchKernelGGL((moe_gate_up_kernel<decltype(fmt)::value, decltype(stream_c)::value,
-                                               decltype(ahead)::value>),
+                                               decltype(ahead)::value, false>),
                            up, dim3(kThreads), 0, stream, p, ws);
         return hipGetLastError();
     };
@@ -691,7 +828,24 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t stream) {
         return ahead ? launch_one(fmt, bool_constant<false>{}, bool_constant<true>{})
                      : launch_one(fmt, bool_constant<false>{}, bool_constant<false>{});
     };
+    // One token, us, against the form for more: 64 experts of 2048 x 1024, 8 a
+    // token, 22.7 / 25.3; 32 of 1040 x 688, 2, 14.4 / 19.2; 16 of 4096 x 2048, 4,
+    // 36.0 / 36.1; 8 of 4096 x 4096, 2, 35.2 / 40.8.  The same form for two tokens,
+    // which read shared experts twice then, 31.0 / 33.3 and 16.3 / 19.6, but 57.1 /
+    // 51.7 and 63.6 / 52.2.
+    auto launch_one = [&](auto fmt) {
+        constexpr int kFmt = decltype(fmt)::value;
+        auto* up_kernel = p.dim % kGroup == 0 ? moe_gate_up_kernel<kFmt, true, true, true>
+                                              : moe_gate_up_kernel<kFmt, false, true, true>;
+        hipLaunchKernelGGL(up_kernel, up, dim3(kThreads), 0, stream, p, ws);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        hipLaunchKernelGGL((moe_down_one_kernel<kFmt>), dim3(p.dim / kOneRows),
+                           dim3(kOneWaves * kWave), 0, stream, p, ws);
+        return hipGetLastError();
+    };
     auto launch = [&](auto fmt) {
+        if (p.tokens == 1) return launch_one(fmt);
         const hipError_t err = pick(gate_up, fmt, p.dim, up);
         return err == hipSuccess ? pick(down_all, fmt, p.hidden, down) : err;
     };

@@ -549,6 +549,26 @@ def test_moe_sizes(f, t, e, k, d, h):
     check_moe(f, t, e, k, d, h, renorm=(t + k) % 2 == 0)
 
 
+@pytest.mark.parametrize("e,k,d,h", [(16, 16, 64, 2064), (16, 9, 48, 16), (12, 5, 272, 144),
+                                     (130, 3, 16, 640), (512, 1, 80, 48), (4, 2, 128, 4096),
+                                     (70, 8, 2048, 256)])
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+def test_moe_one_token(f, e, k, d, h, fmt):
+    check_moe(f, 1, e, k, d, h, fmt=fmt, renorm=k % 2 == 1, seed=e + k)
+
+
+def test_moe_one_token_ties_and_nan(f):
+    e, k, d, h = 70, 4, 128, 32
+    ins = list(moe_inputs(1, e, d, h, E4M3, 5))
+    ins[1] = np.zeros_like(ins[1])  # every logit is 0
+    _, ids, _ = moe_device(f, ins, 1, e, k, d, h, E4M3, True)
+    assert (ids == np.arange(k)).all()
+    ins[0] = np.full_like(ins[0], 0x7FC0)  # a NaN token
+    got, ids, wt = moe_device(f, ins, 1, e, k, d, h, E4M3, True)
+    assert np.isnan(wl.bf16_bits_to_f32(got)).all() and np.isnan(wt).all()
+    assert (ids == np.arange(k)).all()
+
+
 @pytest.mark.parametrize("fmt", [E4M3, E5M2])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_moe_formats(f, fmt, renorm):
