@@ -535,13 +535,13 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
  *
  * in the arithmetic of fp8_quantize_block and fp8_mm_block; x and w are
  * quantized in fmt, g in fmt_g.  Two launches forward and two backward when
- * all three gradients are asked (more for sizes or formats that the tiled
- * products do not take).
+ * all three gradients are asked (more for large sizes, where each product
+ * has its own, and for sizes or formats that the tiled products do not take).
  * w: bf16 [N][K]; or NULL with w8, sw: its codes in fmt_w and the steps of
  *     their tiles, used as they are.
  * saved: device buffer of fp8_linear_block_saved(M, N, K, want_dx, want_dw)
- *     bytes (0: may be NULL), 256-byte aligned: what the forward keeps for the gradients
- *     that a backward will ask; the same flags go to both calls.  A weight
+ *     bytes (0: may be NULL), 256-byte aligned: what the forward keeps for
+ *     the gradients that a backward will ask; the same flags go to both calls.  A weight
  *     given as codes is not kept: give want_dx 0 to the size, and w8, sw to
  *     the backward.
  * workspace: fp8_linear_block_fwd_workspace / _bwd_workspace(M, N, K) bytes,
