@@ -340,3 +340,11 @@ def test_block_recipe():
         with pytest.raises(ValueError, match="bf16 bias"):
             ac.fp8_linear(x, w8, w_scale=torch.ones(2, 3), b_scale=torch.ones(1),
                           bias=torch.zeros(256, dtype=torch.uint8).view(torch.float8_e4m3fn))
+
+
+def test_expert_module_refuses_host_tensors():
+    from fp8_tensor_scaled_amd.moe import FP8MoE
+    b16 = torch.bfloat16
+    with pytest.raises(ValueError, match="router must be a 2-D bfloat16 tensor on the GPU"):
+        FP8MoE(torch.zeros(4, 64, dtype=b16), torch.zeros(4, 64, 64, dtype=b16),
+               torch.zeros(4, 64, 32, dtype=b16), 2)
