@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -230,6 +231,22 @@ def _stream(stream=None):
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+# One lock per (device index, stream handle).  A library call enqueues several
+# launches that hand data on through a workspace, with the interpreter lock
+# released, and threads share streams (the default one is every thread's
+# current stream): whoever keeps a workspace per stream holds the stream's lock
+# from taking it until the call returns, so that calls on it follow each other.
+# (Reentrant: a call made inside, by a finalizer say, is enqueued as a whole
+# before the outer one.)
+_STREAM_LOCKS: dict = {}
+
+
+def _stream_lock(device: torch.device, stream):
+    key = (device.index, stream.value)
+    lock = _STREAM_LOCKS.get(key)
+    return _STREAM_LOCKS.setdefault(key, threading.RLock()) if lock is None else lock
 
 
 class Ring:

@@ -51,6 +51,7 @@ import torch
 
 from . import (E4M3, E5M2, OUT_BF16, Ring, _groups, _linear_block_bwd_call,
                _linear_block_fwd_call, _linear_bwd_call, _linear_fwd_call, _stream,
+               _stream_lock,
                fp8_colsum, fp8_colsum_workspace,
                fp8_linear_block_bwd_workspace, fp8_linear_block_fwd_workspace,
                fp8_linear_block_saved,
@@ -196,7 +197,8 @@ class fp8_autocast:
 # call on that stream, forward and backward, of any shape: it grows (a new
 # zero-filled buffer replaces it) when a call needs more, and never holds
 # more than the largest call on that stream asked for.  Calls on one stream
-# are ordered, so they never use it at the same time.
+# are ordered, and a call is enqueued as a whole (under the stream's lock,
+# whichever thread makes it), so they never use it at the same time.
 _WS: dict = {}
 
 
@@ -259,10 +261,11 @@ class _LinearFp8(torch.autograd.Function):
         if recipe.dynamic:
             ctx.meta = None
             # buffers sized from the operands here, so the unchecked call
-            _linear_fwd_call(x2.view(torch.int16), w.view(torch.int16), bias16, M, N, K, fmt,
-                             True, recipe.margin, None, None,
-                             _workspace(dev, _ws_sizes(M, N, K)[0]), scales,
-                             out.view(torch.int16), None, E5M2, None, None)
+            with _stream_lock(dev, _stream()):
+                _linear_fwd_call(x2.view(torch.int16), w.view(torch.int16), bias16, M, N, K, fmt,
+                                 True, recipe.margin, None, None,
+                                 _workspace(dev, _ws_sizes(M, N, K)[0]), scales,
+                                 out.view(torch.int16), None, E5M2, None, None)
             ctx.save_for_backward(x2, w, scales)
             return out.reshape(*x.shape[:-1], N)
         meta = ctx.meta = _STATE.get_weight_meta(w, recipe)
@@ -278,9 +281,10 @@ class _LinearFp8(torch.autograd.Function):
             # wanted; it seeds, folds and advances the rings
             x8b = torch.empty(M * K, dtype=torch.uint8, device=dev) if need_w else None
             w8b = torch.empty(N * K, dtype=torch.uint8, device=dev) if need_x else None
-            _linear_fwd_call(xi, wi, bias16, M, N, K, fmt, False, m, meta.x, meta.w,
-                             _workspace(dev, _ws_sizes(M, N, K)[0]), scales,
-                             out.view(torch.int16), None, ctx.fmt_bwd, x8b, w8b)
+            with _stream_lock(dev, _stream()):
+                _linear_fwd_call(xi, wi, bias16, M, N, K, fmt, False, m, meta.x, meta.w,
+                                 _workspace(dev, _ws_sizes(M, N, K)[0]), scales,
+                                 out.view(torch.int16), None, ctx.fmt_bwd, x8b, w8b)
             ctx.save_for_backward(x8b, w8b, scales)
             return out.reshape(*x.shape[:-1], N)
         # one format both ways: the forward's codes are the backward's
@@ -316,18 +320,20 @@ class _LinearFp8(torch.autograd.Function):
         fmt, m = ctx.fmt_bwd, ctx.recipe.margin
         if ctx.meta is None:
             x2, w, scales = ctx.saved_tensors
-            _linear_bwd_call(i16(g2), i16(x2), i16(w), M, N, K, fmt, True, m, scales, None,
-                             _workspace(dev, _ws_sizes(M, N, K)[1]), None, i16(dx), i16(dw),
-                             i16(db), None, None, None)
+            with _stream_lock(dev, _stream()):
+                _linear_bwd_call(i16(g2), i16(x2), i16(w), M, N, K, fmt, True, m, scales, None,
+                                 _workspace(dev, _ws_sizes(M, N, K)[1]), None, i16(dx), i16(dw),
+                                 i16(db), None, None, None)
         else:
             # the forward kept x8b when dW is wanted and w8b when dX is; the
             # call seeds, uses and advances the g ring
             x8b, w8b, scales = ctx.saved_tensors
-            _linear_bwd_call(i16(g2), None, None, M, N, K, fmt, False, m, scales, ctx.meta.g,
-                             _workspace(dev, _ws_sizes(M, N, K)[2]), None,
-                             i16(dx), i16(dw), i16(db), None,
-                             x8b if dw is not None else None,
-                             w8b if dx is not None else None)
+            with _stream_lock(dev, _stream()):
+                _linear_bwd_call(i16(g2), None, None, M, N, K, fmt, False, m, scales, ctx.meta.g,
+                                 _workspace(dev, _ws_sizes(M, N, K)[2]), None,
+                                 i16(dx), i16(dw), i16(db), None,
+                                 x8b if dw is not None else None,
+                                 w8b if dx is not None else None)
         return (None if dx is None else dx.reshape(ctx.x_shape), dw, db, None, None)
 
 
@@ -470,10 +476,12 @@ class _LinearFp8Block(torch.autograd.Function):
             if need:
                 saved = torch.empty(need, dtype=torch.uint8, device=dev)
             # buffers sized from the operands here, so the unchecked call
-            ws = _workspace(dev, _block_ws_sizes(M, N, K)[0])
-            _linear_block_fwd_call(x2, None if codes else w, bias, M, N, K, fmt, margin, saved,
-                                   need, want_dx, want_dw, ws, ws.numel(), out,
-                                   w if codes else None, w_scale, ctx.conf[8], _stream())
+            stream = _stream()
+            with _stream_lock(dev, stream):
+                ws = _workspace(dev, _block_ws_sizes(M, N, K)[0])
+                _linear_block_fwd_call(x2, None if codes else w, bias, M, N, K, fmt, margin, saved,
+                                       need, want_dx, want_dw, ws, ws.numel(), out,
+                                       w if codes else None, w_scale, ctx.conf[8], stream)
         ctx.save_for_backward(saved, w if codes else None, w_scale)
         return out if x.dim() == 2 else out.reshape(*x.shape[:-1], N)
 
@@ -490,10 +498,12 @@ class _LinearFp8Block(torch.autograd.Function):
         db = make(N, dtype=b16, device=dev) if need_b else None
         if M > 0 and (need_x or need_w or need_b):
             g2 = _bf16(g.reshape(-1, N), "the output gradient")
-            ws = _workspace(dev, _block_ws_sizes(M, N, K)[1])
-            _linear_block_bwd_call(g2, saved, 0 if saved is None else saved.numel(), M, N, K, fmt,
-                                   fmt_g, margin, want_dx, want_dw, ws, ws.numel(), dx, dw, db,
-                                   w8, sw, fmt_w, _stream())
+            stream = _stream()
+            with _stream_lock(dev, stream):
+                ws = _workspace(dev, _block_ws_sizes(M, N, K)[1])
+                _linear_block_bwd_call(g2, saved, 0 if saved is None else saved.numel(), M, N, K,
+                                       fmt, fmt_g, margin, want_dx, want_dw, ws, ws.numel(), dx,
+                                       dw, db, w8, sw, fmt_w, stream)
         if dx is not None and len(ctx.x_shape) != 2:
             dx = dx.reshape(ctx.x_shape)
         return dx, dw, None, db, None, None

@@ -11,7 +11,8 @@ from __future__ import annotations
 
 import torch
 
-from . import E4M3, E5M2, _groups, _stream, fp8_moe, fp8_moe_workspace, fp8_quantize_block
+from . import (E4M3, E5M2, _groups, _stream, _stream_lock, fp8_moe, fp8_moe_workspace,
+               fp8_quantize_block)
 
 __all__ = ["FP8MoE"]
 
@@ -25,7 +26,7 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
         # Cleared within the graph, whose memory it is: every replay finds it
         # as its first use needs it, and no eager call finds it uncleared.
         return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, _stream().value)  # calls on one stream follow each other
+    key = (dev.index, _stream().value)  # (its lock is held: see _stream_lock)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _WS[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
@@ -92,7 +93,9 @@ class FP8MoE(torch.nn.Module):
             for at in range(0, x2.shape[0], _MAX_TOKENS):
                 xs, ys = x2[at:at + _MAX_TOKENS], out[at:at + _MAX_TOKENS]
                 n = xs.shape[0]
-                ws = _workspace(x.device, fp8_moe_workspace(n, experts, self.top_k, dim, hidden))
-                fp8_moe(xs, self.router, self.w13, self.w13_steps, self.w2, self.w2_steps, n,
-                        experts, self.top_k, dim, hidden, self.fmt, self.renormalize, ws, ys)
+                need = fp8_moe_workspace(n, experts, self.top_k, dim, hidden)
+                with _stream_lock(x.device, _stream()):
+                    fp8_moe(xs, self.router, self.w13, self.w13_steps, self.w2, self.w2_steps, n,
+                            experts, self.top_k, dim, hidden, self.fmt, self.renormalize,
+                            _workspace(x.device, need), ys)
         return out.reshape(x.shape)
