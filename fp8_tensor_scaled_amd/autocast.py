@@ -199,7 +199,14 @@ class fp8_autocast:
 # more than the largest call on that stream asked for.  Calls on one stream
 # are ordered, and a call is enqueued as a whole (under the stream's lock,
 # whichever thread makes it), so they never use it at the same time.
+#
+# A captured call gets a buffer of its own, from the graph's memory, with the
+# control block cleared inside the graph: a kept one would be cleared by the
+# replays only, not for the eager calls after the capture, and could be
+# replaced by a larger one (its memory given away) while replays still write
+# to it.
 _WS: dict = {}
+_CONTROL = 6656  # bytes of the control block
 
 
 @functools.lru_cache(maxsize=256)
@@ -210,7 +217,14 @@ def _ws_sizes(M: int, N: int, K: int) -> tuple:
             fp8_linear_bwd_workspace_codes(M, N, K))
 
 
-def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
+def _workspace(dev: torch.device, nbytes: int, control: bool = True) -> torch.Tensor:
+    """The workspace of a call on the current stream; control: whether the
+    call uses the control block (block scaling has none)."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if control:
+            ws[:_CONTROL].zero_()
+        return ws
     key = (dev.index, _stream().value)  # the stream the library call will use
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -478,7 +492,7 @@ class _LinearFp8Block(torch.autograd.Function):
             # buffers sized from the operands here, so the unchecked call
             stream = _stream()
             with _stream_lock(dev, stream):
-                ws = _workspace(dev, _block_ws_sizes(M, N, K)[0])
+                ws = _workspace(dev, _block_ws_sizes(M, N, K)[0], control=False)
                 _linear_block_fwd_call(x2, None if codes else w, bias, M, N, K, fmt, margin, saved,
                                        need, want_dx, want_dw, ws, ws.numel(), out,
                                        w if codes else None, w_scale, ctx.conf[8], stream)
@@ -500,7 +514,7 @@ class _LinearFp8Block(torch.autograd.Function):
             g2 = _bf16(g.reshape(-1, N), "the output gradient")
             stream = _stream()
             with _stream_lock(dev, stream):
-                ws = _workspace(dev, _block_ws_sizes(M, N, K)[1])
+                ws = _workspace(dev, _block_ws_sizes(M, N, K)[1], control=False)
                 _linear_block_bwd_call(g2, saved, 0 if saved is None else saved.numel(), M, N, K,
                                        fmt, fmt_g, margin, want_dx, want_dw, ws, ws.numel(), dx,
                                        dw, db, w8, sw, fmt_w, stream)
