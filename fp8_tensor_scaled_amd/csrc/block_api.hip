@@ -237,6 +237,10 @@ fp8_status_t check_layer(const char* who, int64_t M, int64_t N, int64_t K, int32
     if (M < 1 || N < 1 || K < 1)
         return fail(FP8_EINVAL, "%s: M, N, K must be >= 1 (got %lld, %lld, %lld)", who,
                     (long long)M, (long long)N, (long long)K);
+    // N and K are row strides of the products' operands (see fp8_mm_block)
+    if (N >= (1 << 24) || K >= (1 << 24))
+        return fail(FP8_EINVAL, "%s: N and K must be below 2^24 (got %lld, %lld)", who,
+                    (long long)N, (long long)K);
     const double lim = 1099511627776.0;
     if ((double)M * N >= lim || (double)M * K >= lim || (double)N * K >= lim)
         return fail(FP8_EINVAL, "%s: a matrix is too large", who);

@@ -534,7 +534,8 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
  *   db[N]     = bf16( sum_m g[m][:] )
  *
  * in the arithmetic of fp8_quantize_block and fp8_mm_block; x and w are
- * quantized in fmt, g in fmt_g.  Two launches forward and two backward when
+ * quantized in fmt, g in fmt_g.  N, K < 2^24 (they are the products' row
+ * strides).  Two launches forward and two backward when
  * all three gradients are asked (more for large sizes, where each product
  * has its own, and for sizes or formats that the tiled products do not take).
  * w: bf16 [N][K]; or NULL with w8, sw: its codes in fmt_w and the steps of
