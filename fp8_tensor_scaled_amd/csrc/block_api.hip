@@ -48,6 +48,8 @@ fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, i
     if (!x) return fail(FP8_EINVAL, "%s: x is NULL", who);
     if ((uintptr_t)x % (in_type == FP8_IN_F32 ? 4 : 2))
         return fail(FP8_EINVAL, "%s: x is not aligned to its elements", who);
+    if (((uintptr_t)scale_row | (uintptr_t)scale_col | (uintptr_t)scale_tile) & 3)
+        return fail(FP8_EINVAL, "%s: a scale is not aligned to its elements", who);
     if ((double)groups_of(rows) * (double)groups_of(cols) >= 2147483647.0)
         return fail(FP8_EINVAL, "%s: too many blocks", who);
     if (out_row && out_col) {
@@ -254,6 +256,14 @@ fp8_status_t check_layer(const char* who, int64_t M, int64_t N, int64_t K, int32
     return FP8_OK;
 }
 
+// The bf16 operands' addresses (or'ed) and the steps' of a weight given as codes.
+fp8_status_t check_aligned(const char* who, uintptr_t bf16, const float* steps) {
+    if (bf16 & 1) return fail(FP8_EINVAL, "%s: a bf16 operand is not aligned to its elements", who);
+    if ((uintptr_t)steps & 3)
+        return fail(FP8_EINVAL, "%s: sw is not aligned to its elements", who);
+    return FP8_OK;
+}
+
 fp8_status_t check_scratch(const char* who, const char* what, const void* p, size_t have,
                            size_t need) {
     if (need == 0) return FP8_OK;
@@ -332,6 +342,9 @@ fp8_status_t fp8_linear_block_fwd(const uint16_t* x, const uint16_t* w, const ui
     if (w8 && !sw) return fail(FP8_EINVAL, "%s: codes of the weight need their steps", who);
     fp8_status_t st = check_layer(who, M, N, K, margin);
     if (st) return st;
+    if ((st = check_aligned(who, (uintptr_t)x | (uintptr_t)w | (uintptr_t)bias | (uintptr_t)out,
+                            w8 ? sw : nullptr)))
+        return st;
     // a weight given as codes is its caller's to keep
     const SavedLayout S = saved_layout(M, N, K, want_dx && w, want_dw != 0);
     if ((st = check_scratch(who, "saved", saved, saved_bytes, S.total))) return st;
@@ -381,6 +394,9 @@ fp8_status_t fp8_linear_block_bwd(const uint16_t* g, const void* saved, size_t s
     if (w8 && !sw) return fail(FP8_EINVAL, "%s: codes of the weight need their steps", who);
     fp8_status_t st = check_layer(who, M, N, K, margin);
     if (st) return st;
+    if ((st = check_aligned(who, (uintptr_t)g | (uintptr_t)dx | (uintptr_t)dw | (uintptr_t)db,
+                            w8 ? sw : nullptr)))
+        return st;
     if ((dx && !w8 && !want_dx) || (dw && !want_dw))
         return fail(FP8_EINVAL, "%s: a gradient whose codes the forward did not keep", who);
     const SavedLayout S = saved_layout(M, N, K, want_dx && !w8, want_dw != 0);

@@ -43,3 +43,25 @@ def test_layer_row_strides(backward, M, N, K):
     kernel reaches a tile's rows (up to 127 of them) by 32-bit offsets: as
     fp8_mm_block, below 2^24."""
     assert call(backward)(*layer_args(M, N, K, backward)) == 1 and "below 2^24" in err(), err()
+
+
+ODD, HALF = P(0x1001), P(0x1002)  # not aligned to bf16, to fp32
+
+
+@pytest.mark.parametrize("backward,over", [
+    (False, dict(x=ODD)), (False, dict(w=ODD)), (False, dict(bias=ODD)), (False, dict(out=ODD)),
+    (False, dict(w=None, w8=FAKE, sw=HALF)), (True, dict(g=ODD)), (True, dict(dx=ODD)),
+    (True, dict(dw=ODD)), (True, dict(db=ODD)), (True, dict(w8=FAKE, sw=HALF))])
+def test_layer_alignment(backward, over):
+    """The steps of a weight's tiles are loaded into LDS by whole dwords."""
+    args = layer_args(4, 200, 300, backward, **over)
+    assert call(backward)(*args) == 1 and "aligned to its elements" in err(), err()
+
+
+@pytest.mark.parametrize("steps", ["scale_row", "scale_col", "scale_tile"])
+def test_quantize_alignment(steps):
+    a = dict(x=FAKE, in_type=0, rows=4, cols=200, ldx=200, fmt=0, margin=0, out_row=None,
+             scale_row=None, out_col=None, scale_col=None, out_tile=None, scale_tile=None,
+             stream=None)
+    a.update({steps: HALF, steps.replace("scale", "out"): FAKE})
+    assert f._lib.fp8_quantize_block(*a.values()) == 1 and "aligned to its elements" in err(), err()
