@@ -603,11 +603,15 @@ __global__ __launch_bounds__(kThreads) void moe_gate_up_kernel(MoeLaunch p, MoeW
 #pragma unroll
             for (int i = 0; i < kHalf; ++i) {
                 const float h = v[i] / (1.0f + expf(-v[i])) * v[kHalf + i];
-                const uint16_t hi = f32_to_bf16(h);
+                // Finite values that round past bf16's largest keep that and the
+                // rest; an infinite one has no rest (inf - inf is NaN).
+                const bool inf = fabsf(h) == INFINITY;
+                uint16_t hi = f32_to_bf16(h);
+                if ((hi & 0x7fff) == 0x7f80 && !inf) --hi;
                 if (f0 + 16 * i < p.hidden) {
                     uint16_t* at = row + moe_h_place(f0 + 16 * i + tid % 16);
                     at[0] = hi;
-                    at[kGroup] = f32_to_bf16(h - bf16_to_f32(hi));
+                    at[kGroup] = inf ? 0 : f32_to_bf16(h - bf16_to_f32(hi));
                 }
             }
         }
