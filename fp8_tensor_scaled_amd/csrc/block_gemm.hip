@@ -315,7 +315,8 @@ static bool tiled_supported(const BlockGemmLaunch& g) {
     if ((double)(g.trans_a ? g.k : g.m) * (double)g.lda >= lim) return false;
     if ((double)(g.trans_b ? g.n : g.k) * (double)g.ldb >= lim) return false;
     if ((double)g.sa.sk >= lim / 4 || (double)g.sb.sk >= lim / 4) return false;
-    return (double)((g.m + 63) / 64) * (double)((g.n + 63) / 64) < lim;
+    // a grid dimension counts lanes in 32 bits: fewer than 2^23 workgroups of 512
+    return (double)((g.m + 127) / 128) * (double)((g.n + 127) / 128) < 8388608.0;
 }
 
 // A backward's products go in one launch of 128 x 128 tiles up to this many of

@@ -42,6 +42,7 @@ struct BlockQuantParams {
     float* scale_tile;
     float* sums;  // [groups_of(rows)][cols] column sums of x over each 128 rows
     int64_t col_groups;
+    int64_t bands;  // workgroups of the launch (see grid_of)
     int vec_out;  // codes go out 8 at a time: cols % 8 == 0 and aligned outputs
 };
 
@@ -300,26 +301,38 @@ __device__ __forceinline__ void quantize_band(const BlockQuantParams& p, int64_t
     }
 }
 
+// Workgroups in a grid: past kGridX of them by rows of kGridX.  (A grid dimension
+// counts lanes in 32 bits: 2^24 workgroups of 256 lanes would be none.)
+constexpr int64_t kGridX = 1 << 21;
+dim3 grid_of(int64_t workgroups) {
+    if (workgroups <= kGridX) return dim3((unsigned)workgroups);
+    return dim3((unsigned)kGridX, (unsigned)((workgroups + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t workgroup_id() {
+    return (int64_t)blockIdx.y * kGridX + blockIdx.x;
+}
+
 template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM, int T, int P>
 __global__ __launch_bounds__(T) void quantize_block_kernel(BlockQuantParams p) {
     __shared__ QuantLds<T> lds;
-    quantize_band<IN, FMT, ROW, COL, TILE, SUM, T, P>(
-        p, (int64_t)blockIdx.x % p.col_groups, (int64_t)blockIdx.x / p.col_groups, lds);
+    const int64_t id = workgroup_id();
+    if (id >= p.bands) return;
+    quantize_band<IN, FMT, ROW, COL, TILE, SUM, T, P>(p, id % p.col_groups, id / p.col_groups, lds);
 }
 
 // The layer's forward: x by rows (and columns, WITH_COL) and w by tiles in
 // one launch, x's bands first.
 template <int FMT, bool WITH_COL, int T, int P>
 __global__ __launch_bounds__(T) void quantize_block_two_kernel(BlockQuantParams px,
-                                                              BlockQuantParams pw, int nx) {
+                                                              BlockQuantParams pw) {
     __shared__ QuantLds<T> lds;
-    if ((int)blockIdx.x < nx)
+    const int64_t id = workgroup_id(), of_w = id - px.bands;
+    if (of_w < 0)
         quantize_band<kInBf16, FMT, true, WITH_COL, false, false, T, P>(
-            px, (int64_t)blockIdx.x % px.col_groups, (int64_t)blockIdx.x / px.col_groups, lds);
-    else
+            px, id % px.col_groups, id / px.col_groups, lds);
+    else if (of_w < pw.bands)
         quantize_band<kInBf16, FMT, false, false, true, false, T, P>(
-            pw, (int64_t)(blockIdx.x - nx) % pw.col_groups,
-            (int64_t)(blockIdx.x - nx) / pw.col_groups, lds);
+            pw, of_w % pw.col_groups, of_w / pw.col_groups, lds);
 }
 
 BlockQuantParams params_of(const BlockQuantLaunch& q) {
@@ -337,6 +350,7 @@ BlockQuantParams params_of(const BlockQuantLaunch& q) {
     p.scale_tile = q.scale_tile;
     p.sums = q.sums;
     p.col_groups = groups_of(q.cols);
+    p.bands = groups_of(q.rows) * p.col_groups;
     const uintptr_t outs = reinterpret_cast<uintptr_t>(q.out_row) |
                            reinterpret_cast<uintptr_t>(q.out_col) |
                            reinterpret_cast<uintptr_t>(q.out_tile);
@@ -353,22 +367,23 @@ BlockQuantParams params_of(const BlockQuantLaunch& q) {
 constexpr int64_t kManyTiles = 512;
 
 template <int IN, int FMT, bool ROW, bool COL, bool TILE, bool SUM>
-hipError_t launch_kinds(const BlockQuantParams& p, hipStream_t stream) {
-    const int64_t tiles = groups_of(p.rows) * p.col_groups;
+hipError_t launch_kinds(BlockQuantParams p, hipStream_t stream) {
+    const int64_t tiles = p.bands;
     if constexpr (ROW && !COL && !SUM) {
-        if (tiles < kManyTiles)
+        if (tiles < kManyTiles) {
+            p.bands = (p.rows + 15) / 16 * p.col_groups;
             hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, true, false, false, false, 256, 1>),
-                               dim3((unsigned)((p.rows + 15) / 16 * p.col_groups)), dim3(256), 0,
-                               stream, p);
-        else
+                               grid_of(p.bands), dim3(256), 0, stream, p);
+        } else {
             hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, true, false, false, false, 256, 8>),
-                               dim3((unsigned)tiles), dim3(256), 0, stream, p);
+                               grid_of(tiles), dim3(256), 0, stream, p);
+        }
     } else if (tiles < kManyTiles) {
         hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, ROW, COL, TILE, SUM, 1024, 2>),
-                           dim3((unsigned)tiles), dim3(1024), 0, stream, p);
+                           grid_of(tiles), dim3(1024), 0, stream, p);
     } else {
         hipLaunchKernelGGL((quantize_block_kernel<IN, FMT, ROW, COL, TILE, SUM, 256, 8>),
-                           dim3((unsigned)tiles), dim3(256), 0, stream, p);
+                           grid_of(tiles), dim3(256), 0, stream, p);
     }
     return hipGetLastError();
 }
@@ -386,15 +401,13 @@ hipError_t launch_in(const BlockQuantParams& p, hipStream_t stream) {
 
 template <int FMT, bool WITH_COL>
 hipError_t launch_two(const BlockQuantParams& px, const BlockQuantParams& pw, hipStream_t stream) {
-    const int64_t nx = groups_of(px.rows) * px.col_groups;
-    const int64_t nw = groups_of(pw.rows) * pw.col_groups;
-    const dim3 grid((unsigned)(nx + nw));
-    if (nx + nw < kManyTiles)
-        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 1024, 2>), grid, dim3(1024), 0,
-                           stream, px, pw, (int)nx);
+    const int64_t tiles = px.bands + pw.bands;
+    if (tiles < kManyTiles)
+        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 1024, 2>), grid_of(tiles),
+                           dim3(1024), 0, stream, px, pw);
     else
-        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 256, 8>), grid, dim3(256), 0,
-                           stream, px, pw, (int)nx);
+        hipLaunchKernelGGL((quantize_block_two_kernel<FMT, WITH_COL, 256, 8>), grid_of(tiles),
+                           dim3(256), 0, stream, px, pw);
     return hipGetLastError();
 }
 
