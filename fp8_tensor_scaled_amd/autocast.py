@@ -37,6 +37,7 @@ weight may come with an fp8 bias of the same format and its step
 
 The backward reads everything it needs from the forward's context, so it
 runs in fp8 wherever ``backward()`` is called, inside the region or not.
+It is defined once: a second derivative through it raises.
 """
 
 from __future__ import annotations
@@ -241,6 +242,36 @@ def _bf16(t: torch.Tensor | None, what: str) -> torch.Tensor | None:
     return t.contiguous()
 
 
+class _Undefined(torch.autograd.Function):
+    """A gradient as it is; its own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, grad, *of):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("fp8_linear can be differentiated once: the second derivative of an "
+                           "fp8 layer is not defined")
+
+
+def _once(backward):
+    """Marks a backward whose gradients come from library calls, which autograd
+    would take for constants: differentiating them again raises, whether it is
+    for the output's gradient, for a leaf among the inputs or for everything.
+    (torch's own once_differentiable only sees the first.)"""
+    @functools.wraps(backward)
+    def marked(ctx, *g):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *g)
+        with torch.no_grad():
+            grads = backward(ctx, *g)
+        of = [torch.empty(0, requires_grad=True), *g]
+        of += [node.variable for node, _ in ctx.next_functions if hasattr(node, "variable")]
+        return tuple(None if t is None else _Undefined.apply(t, *of) for t in grads)
+    return marked
+
+
 class _LinearFp8(torch.autograd.Function):
     """y[..., N] = x[..., K] w[N][K]^T + b and its gradients in fp8 ([CMP]
     fp8.py _LinearFp8).
@@ -320,6 +351,7 @@ class _LinearFp8(torch.autograd.Function):
         return out.reshape(*x.shape[:-1], N)
 
     @staticmethod
+    @_once
     def backward(ctx, g):
         M, N, K = ctx.mnk
         g2 = _bf16(g.reshape(-1, N), "the output gradient")
@@ -399,6 +431,7 @@ class _LinearFp8Weight(torch.autograd.Function):
         return out.reshape(*x.shape[:-1], N)
 
     @staticmethod
+    @_once
     def backward(ctx, g):
         w8, w_scale = ctx.saved_tensors
         N, K = w8.shape
@@ -500,6 +533,7 @@ class _LinearFp8Block(torch.autograd.Function):
         return out if x.dim() == 2 else out.reshape(*x.shape[:-1], N)
 
     @staticmethod
+    @_once
     def backward(ctx, g):
         M, N, K, fmt, fmt_g, margin, want_dx, want_dw, fmt_w = ctx.conf
         saved, w8, sw = ctx.saved_tensors
