@@ -68,7 +68,7 @@ class FP8MoE(torch.nn.Module):
         if dim % 16 or hidden % 16:
             raise ValueError(f"FP8MoE: dim {dim} and hidden {hidden} must be multiples of 16")
         self.top_k, self.renormalize, self.fmt = int(top_k), bool(renormalize), fmt
-        # (codes as uint8, which a module's .to(dtype) leaves alone)
+        # (codes as uint8, which a module's .to(dtype) leaves alone; _apply keeps the rest)
         with torch.cuda.device(router.device):
             w13_codes, w13_steps = _tile_codes(w13.detach().contiguous(), fmt)
             w2_codes, w2_steps = _tile_codes(w2.detach().contiguous(), fmt)
@@ -77,6 +77,18 @@ class FP8MoE(torch.nn.Module):
         self.register_buffer("w13_steps", w13_steps)
         self.register_buffer("w2", w2_codes)
         self.register_buffer("w2_steps", w2_steps)
+
+    def _apply(self, fn, recurse=True):
+        """Moves follow the model; a conversion of its types (``.half()``,
+        ``.to(torch.float32)``) leaves the router and the steps, whose types
+        the library call asks for, as they were."""
+        before = dict(self._buffers)
+        super()._apply(fn, recurse)
+        for name, old in before.items():
+            new = self._buffers[name]
+            if old is not None and new.dtype != old.dtype:
+                self._buffers[name] = old.to(new.device)
+        return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         experts, dim = self.router.shape
