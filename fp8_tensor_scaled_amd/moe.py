@@ -100,6 +100,8 @@ class FP8MoE(torch.nn.Module):
             raise ValueError("FP8MoE: no gradient is defined; call it under torch.no_grad()")
         hidden = self.w2.shape[2]
         x2 = x.contiguous().reshape(-1, dim)
+        if x2.data_ptr() % 16:  # a view that begins inside a buffer; the call wants whole 16 bytes
+            x2 = x2.clone()
         out = torch.empty_like(x2)
         with torch.cuda.device(x.device):
             for at in range(0, x2.shape[0], _MAX_TOKENS):
