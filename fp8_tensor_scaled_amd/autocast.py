@@ -510,9 +510,10 @@ class _LinearFp8Block(torch.autograd.Function):
         dev = x.device
         margin, fmt = cfg.recipe.margin, cfg.fp8_format.fwd()
         codes = w.dtype in _FP8_DTYPES
-        # (a weight that comes as codes is not copied into what is kept)
+        # (a weight that comes as codes is not copied into what is kept, and takes
+        # no gradient, also where it is a Parameter)
         want_dx = grad_enabled and ctx.needs_input_grad[0] and not codes
-        want_dw = grad_enabled and ctx.needs_input_grad[1]
+        want_dw = grad_enabled and ctx.needs_input_grad[1] and not codes
         ctx.conf = (M, N, K, fmt, cfg.fp8_format.bwd(), margin, want_dx, want_dw,
                     _FP8_DTYPES[w.dtype] if codes else fmt)
         ctx.has_bias, ctx.x_shape = bias is not None, x.shape
@@ -538,7 +539,7 @@ class _LinearFp8Block(torch.autograd.Function):
         M, N, K, fmt, fmt_g, margin, want_dx, want_dw, fmt_w = ctx.conf
         saved, w8, sw = ctx.saved_tensors
         need_x, need_w, _, need_b = ctx.needs_input_grad[:4]
-        need_b = need_b and ctx.has_bias
+        need_w, need_b = need_w and w8 is None, need_b and ctx.has_bias
         dev, b16 = g.device, torch.bfloat16
         make = torch.zeros if M == 0 else torch.empty
         dx = make((M, K), dtype=b16, device=dev) if need_x else None
