@@ -187,25 +187,24 @@ __device__ __forceinline__ Choice select_experts(const MoeLaunch& p, float (&v)[
     for (int i = 0; i < PER; ++i)
         if (lane * PER + i < p.experts) sum += expf(v[i] - mx);
     sum = reduce_sum(sum);
-    // A NaN logit ranks with -inf, below every number; what is taken, and
-    // what is no expert, ranks below that.
-    const float taken = -INFINITY;
-    uint32_t left = 0;  // bit i: expert i of this lane can still be taken
-    bool nan[PER];
+    // Bit i: expert i of this lane can still be taken; its logit is NaN.  Those
+    // rank below every number, -inf too: they come when no other is left.
+    uint32_t left = 0, nan = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        nan[i] = v[i] != v[i];
-        if (nan[i]) v[i] = taken;
+        if (v[i] != v[i]) nan |= 1u << i, v[i] = -INFINITY;
         if (lane * PER + i < p.experts) left |= 1u << i;
     }
     float chosen = -INFINITY;  // lane j's: the j-th expert's logit, and its index
     int chosen_id = 0;
     for (int j = 0; j < p.top_k; ++j) {
+        uint32_t can = left & ~nan;
+        if (__ballot(can != 0) == 0) can = left;
         float best = -INFINITY;
         int at = -1;
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i)
-            if ((left >> i & 1) && (at < 0 || v[i] >= best)) best = v[i], at = i;
+            if ((can >> i & 1) && (at < 0 || v[i] >= best)) best = v[i], at = i;
         const float top = reduce_max(best);
         const uint64_t who = __ballot(at >= 0 && best == top);
         const int winner = __ffsll((unsigned long long)who) - 1;
@@ -213,7 +212,7 @@ __device__ __forceinline__ Choice select_experts(const MoeLaunch& p, float (&v)[
         float value = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (i == at) value = nan[i] ? NAN : v[i];
+            if (i == at) value = nan >> i & 1 ? NAN : v[i];
         const int id = __builtin_amdgcn_readlane(lane * PER + at, winner);
         value = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), winner));
         if (mine) left &= ~(1u << at);
