@@ -270,23 +270,24 @@ def check_against_linear_entry_points(f, torch):
 # (KiB per dispatch, one counter per run, `bench.py --kernel NAME`), scaled by
 # what the same counters read for a 192 MiB copy (FETCH_SIZE x 2.0, WRITE_SIZE
 # x 1.0).  Valid only for the kernel code they were taken on: PMC_SRC is the
-# sha256 of gemm_tiled.hip + common.hpp with comments and blank lines left out
+# sha256 of PMC_SOURCES with comments and blank lines left out
 # (gemm_source_hash); any other code gives null.
+PMC_SOURCES = ("gemm_tiled.hip", "gemm_operand.hpp", "common.hpp")
 PMC_SCALE = {"FETCH_SIZE": 2.0, "WRITE_SIZE": 1.0}
 PMC_TRAFFIC = {
     "gemm_nt_fwd": {"FETCH_SIZE": 49228.5, "WRITE_SIZE": 32768.0},
     "gemm_bwd_pair": {"FETCH_SIZE": 98498.1, "WRITE_SIZE": 65536.0},
 }
-PMC_SRC = "70574c763432b02f895235d5f95f35dbc6d9445aa733830adb213d21d350d7fd"
+PMC_SRC = "595a0b24f88271a8999d941d1b550df020c07ff1d358c1c69d9dd9d381eb5c44"
 
 
 def gemm_source_hash():
-    """sha256 of the GEMM kernels' code: gemm_tiled.hip and common.hpp, each
-    line cut at `//` and stripped, blank lines dropped (the sources have no
-    block comments and no `//` inside literals)."""
+    """sha256 of the GEMM kernels' code: PMC_SOURCES, each line cut at `//` and
+    stripped, blank lines dropped (the sources have no block comments and no
+    `//` inside literals)."""
     import hashlib
     h = hashlib.sha256()
-    for part in ("gemm_tiled.hip", "common.hpp"):
+    for part in PMC_SOURCES:
         with open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "fp8_tensor_scaled_amd",
                                "csrc", part), encoding="utf-8") as fh:
             for line in fh:
