@@ -86,7 +86,8 @@ class FP8Recipe:
     """step = max(peak / FP8_MAX / 2^margin, 1e-12) with peak the max of the
     amax history (delayed), the current amax (dynamic), or the current amax of
     each block (block: activations and gradients in groups of 128 along the
-    product's contraction, weights in 128 x 128 tiles; no history)."""
+    product's contraction, weights in 128 x 128 tiles; no history; the division
+    is a multiplication by the fp32 reciprocal, as in fp8_quantize_block)."""
     history_len: int = 16
     margin: int = 0
     dynamic: bool = False

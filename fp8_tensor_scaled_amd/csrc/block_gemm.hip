@@ -335,7 +335,8 @@ constexpr int kFewTiles = 128;
 // Every configuration runs one workgroup per CU, so a launch costs rounds of
 // 256 tiles times a tile's time.  Those, in thousandths of a 256 x 256 tile's,
 // with a step per tile of B: half as large 570, 128 x 128 350 (us, 256 x 256 /
-// half / 128 x 128: 4096^3 NT 67 / 75 / 88; 3008 x 3008 x 2048 NT 31.0 / 34.9 /
+// half / 128 x 128: 4096^3 NT 67 / 75 / 88 in one run,
+// the first 68 to 71 over several cards; 3008 x 3008 x 2048 NT 31.0 / 34.9 /
 // 35.5; 2048 x 4096 x 4096 NT 54.5 / 38.9 / 44.7; 2048^3 NT - / 17.4 / 15.2).
 // With a step per column of B, which the 256 x 256 tile has no registers for, a
 // 128 x 128 one costs 475 / 675 of the half (2048^3 TN 21.2 / 16.5, 3008 x 3008 x

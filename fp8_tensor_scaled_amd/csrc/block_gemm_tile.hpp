@@ -18,7 +18,10 @@
 //  * The matrix instruction takes the B fragment first, so a lane's 16
 //    values of a tile belong to one row of A: with one step per 128 x 128
 //    tile of B the factor is one number per lane and tile.  With a step per
-//    column (BVEC) each value has a factor of its own: twice the vector work.
+//    column (BVEC) each value has a factor of its own: twice the vector work,
+//    and 16 registers more for every 32 columns of a wave, so that of the
+//    three-stage tiles NT's 128 x 256 spills 15 registers and NN's two 2 and 3,
+//    some of them read back inside the loop.
 //  * The steps come into LDS with the operands.  Where both operands' lie
 //    along k (A's rows, B's tiles) they come for ST stages at a time, with
 //    the first of them (CHUNK): a row's next ones are in the same line, and
@@ -285,7 +288,8 @@ __device__ __forceinline__ void block_gemm_tile(const BlockTileParams& p, int bi
         //
         // 128 sums, 32 partial ones and 48 fragment registers leave about 40
         // for all else, and a register spilled inside the loop would be read
-        // back behind every load in flight: so the fragments' LDS addresses
+        // back behind every load in flight (NT keeps one in memory, stored before
+        // the loop and read after it; NN and TN none): so the fragments' LDS addresses
         // are kept per slot and moved to the other one each stage, and the
         // steps come by 32-bit offsets from descriptors.
         typedef const __attribute__((address_space(3))) v4i lds_v4i;

@@ -2,8 +2,11 @@
 // group of 128 values, along rows (1 x 128), along columns (128 x 1) or for
 // 128 x 128 tiles:
 //     s = max(max |x| * fp32(1 / FMAX) * 2^-margin, 1e-12),   q = enc(x * fp32(1 / s)).
-// (The step takes one multiplication where the per-tensor ring's fold takes a
-// division, once per tensor: the two can differ in the last bit.)
+// (The step takes one multiplication by a rounded reciprocal where the per-tensor
+// ring's fold takes a division, once per tensor: the two can differ in the last
+// bit.  Of 4.2 M normal bf16 values, rows
+// in groups, 5084 E4M3 codes lie on the other side of a tie than with an exact
+// step, 2136 with a divided one; E5M2 4720 and 1168.)
 //
 // A workgroup of T lanes holds a band of 128 columns in registers (lane t:
 // columns 8 (t % 16) .. +7 of rows t / 16 + (T / 16) i, i < P; 128 rows

@@ -5,7 +5,9 @@
 //
 // With few tokens per expert the layer is bound by reading the chosen
 // experts' weights once (3 dim hidden bytes each), so both products are
-// shaped for that:
+// shaped for that.  (An expert's weights are read once for every 16 of its
+// tokens: 8 experts of 2048 x 1024, 2 a token, 256 tokens take 93 us and 1024
+// take 292.)
 //
 //  * The routing launch leaves a list of the experts that were reached and
 //    of each one's tokens, so that a workgroup of the products knows its work
@@ -419,9 +421,12 @@ __device__ __forceinline__ void fp8_to_f32(uint32_t w, float (&f)[4]) {
 //
 // A load takes whole 128-byte lines of 8 rows (lane l: row l % 8, bytes 16 (l / 8)
 // ..); with loads of 16 rows x 64 bytes, as the matrix instruction has them, 64
-// tokens took 124 us instead of 109.  Each weight is read once, so with STREAM
-// past the caches (112 us without); not where kdim is no multiple of 128, since a
-// row's pieces then share lines (13 tokens, 1040 x 688: 25.3 us, 29.0 with).
+// tokens took 124 us instead of 109.  With STREAM the loads go past the caches: a gain
+// where an expert has up to 16 tokens and so each weight is read once (64 tokens,
+// 8 of 64 experts of 2048 x 1024, 100 us, 105 without), a loss where it is read
+// again (64 tokens that all take 8 of 8 experts 84 us, 80 without; 256 tokens, 8 of
+// 64, 272 and 245).  Not where kdim is no multiple of 128, since a row's pieces then
+// share lines (13 tokens, 1040 x 688: 25.3 us, 29.0 with).
 // Between a tile's two loads lanes l and l ^ 8 then exchange halves, by one lane permute
 // per register, so that lane l holds row l % 16 and k = 32 (l / 16) .. + 31 of
 // the block: a reordering of k that the sum does not see.

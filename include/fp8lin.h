@@ -513,7 +513,9 @@ fp8_status_t fp8_quantize_block(const void* x, fp8_in_t in_type, int64_t rows, i
  *     bytes (may be 0), 256-byte aligned, zero before its first use and
  *     left so that it can be reused: with it a product of few outputs and
  *     long k is split along k over more workgroups.  The sums are added in a
- *     fixed order, so a call's result does not vary from run to run.
+ *     fixed order, so a call's result does not vary from run to run.  Calls
+ *     that may overlap (on other streams, or enqueued by other threads at the
+ *     same time) need a workspace each.
  * ------------------------------------------------------------------- */
 typedef enum { FP8_GROUP_LINE = 0, FP8_GROUP_TILE = 1 } fp8_group_t;
 
@@ -547,7 +549,9 @@ fp8_status_t fp8_mm_block(const uint8_t* a, const uint8_t* b, fp8_fmt_t fmt_a, f
  *     the backward.
  * workspace: fp8_linear_block_fwd_workspace / _bwd_workspace(M, N, K) bytes,
  *     256-byte aligned; its first 6656 bytes are left as they are, so that
- *     it can be the per-tensor layer's too.
+ *     it can be the per-tensor layer's too.  A call is several launches:
+ *     calls that may overlap (on other streams, or enqueued by other threads
+ *     at the same time) need one each.
  * dx, dw, db: each NULL to skip that gradient.  bias: bf16 [N] or NULL.
  * ------------------------------------------------------------------- */
 size_t fp8_linear_block_saved(int64_t M, int64_t N, int64_t K, int32_t want_dx, int32_t want_dw);
@@ -591,6 +595,8 @@ fp8_status_t fp8_linear_block_bwd(const uint16_t* g, const void* saved, size_t s
  * its outputs, are NaN.
  * workspace: fp8_moe_workspace(...) bytes of device scratch, 256-byte
  *     aligned, zero before its first use and left so that it can be reused.
+ *     A call is three launches: calls that may overlap (on other streams, or
+ *     enqueued by other threads at the same time) need one each.
  * ids, weights: nullable, [tokens][top_k]: e_j (int32) and w_j (fp32),
  *     largest first.
  * ------------------------------------------------------------------- */
