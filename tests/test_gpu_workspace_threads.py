@@ -77,6 +77,7 @@ def test_block_layers_of_two_shapes():
     check(layer(256, 384, 256, r, 1), layer(64, 1024, 512, r, 9))
 
 
-def test_block_layer_beside_a_tensor_scaled_one():
-    check(layer(256, 384, 256, FP8Recipe(block=True), 1),
-          layer(64, 1024, 512, FP8Recipe(dynamic=True), 9))
+@pytest.mark.parametrize("recipe", [FP8Recipe(dynamic=True), FP8Recipe()],
+                         ids=["dynamic", "delayed"])
+def test_block_layer_beside_a_tensor_scaled_one(recipe):
+    check(layer(256, 384, 256, FP8Recipe(block=True), 1), layer(64, 1024, 512, recipe, 9))
