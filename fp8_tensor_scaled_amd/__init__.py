@@ -10,6 +10,7 @@ torch is used for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -872,9 +873,11 @@ ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
 
 # The operands of a call are checked, and their addresses taken, by one function
 # of a small extension; without it by _take_slow, which is what has to say what is
-# wrong in either case.  Sets of dtypes are bits there.
+# wrong in either case.  Sets of dtypes are bits there.  (It is looked up as a
+# module: `from . import` would be content with the None of an earlier import of
+# this package, before a build.)
 try:
-    from . import _fp8binding
+    _fp8binding = importlib.import_module(__name__ + "._fp8binding")
     _bit_of = _fp8binding.bit_of
 except ImportError:  # (not built: the library itself is looked for at the first call)
     _fp8binding = None
