@@ -10,6 +10,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,7 +25,8 @@ SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_tiled.hip", "gemm_skinny
 # the benchmark's ceiling kernels, a library of their own that only bench.py loads
 BENCH_LIB = os.path.join(HERE, "libfp8bench.so")
 BENCH_SOURCES = ["bench_ref.hip"]
-# the Python binding's operand check, an extension module against torch's headers
+# the Python binding's operand check, an extension module against torch's headers;
+# the package works without it, by the check's Python form
 BINDING_LIB = os.path.join(HERE, "_fp8binding.so")
 BINDING_SOURCE = "binding.cpp"
 ARCH = "gfx950"
@@ -71,7 +73,9 @@ def _build_binding() -> None:
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link libfp8lin.so (and the
     benchmark's reference kernels, libfp8bench.so, and the binding's extension,
-    _fp8binding.so); returns the library's path."""
+    _fp8binding.so); returns the library's path.  An extension that cannot be
+    built (it needs a host compiler, Python's and torch's headers) is a warning:
+    none is left, so that the package takes the Python form of its check."""
     hipcc = _hipcc()
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -91,7 +95,6 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + len(BENCH_SOURCES))) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, SOURCES + BENCH_SOURCES))
-    binding.result()
     for lib, parts in ((LIB, objs[:len(SOURCES)]), (BENCH_LIB, objs[len(SOURCES):])):
         tmp = lib + ".tmp%d" % os.getpid()
         cmd = [hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *parts]
@@ -99,6 +102,13 @@ def build(verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, lib)
+    try:
+        binding.result()
+    except Exception as e:  # noqa: BLE001
+        if os.path.exists(BINDING_LIB):  # (of older sources)
+            os.remove(BINDING_LIB)
+        warnings.warn(f"{os.path.basename(BINDING_LIB)} is not built, its check runs in Python "
+                      f"(about 1 us a call): {e}")
     return LIB
 
 

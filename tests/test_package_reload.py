@@ -1,6 +1,7 @@
 """The package in a tree whose operand-check extension is not built yet, as a
 build finds it: imported without it, loaded again without it and, once it is
-there, with it.  A copy of the package in a process of its own."""
+there, with it; and a build that cannot make the extension.  A copy of the
+package in a process of its own."""
 
 import os
 import shutil
@@ -68,4 +69,34 @@ def test_extension_built_meanwhile(bare):
         importlib.reload(f)
         assert f._take is f._fp8binding.take and f._take is not f._take_slow
         refuses(f)
+    """)
+
+
+@pytest.mark.parametrize("cxx", ["missing", "failing"])
+def test_library_built_without_the_extension(bare, cxx):
+    """A machine without a host compiler, or whose compiler fails: the library is
+    linked, the build says what is missing, an extension of older sources goes
+    and the package takes the Python form.  (hipcc is a stub that makes its
+    output file.)"""
+    for name, text in (("hipcc", "while [ \"$1\" != -o ]; do shift; done; : > \"$2\""),
+                       ("failing", "echo no headers here >&2; exit 1")):
+        (bare / name).write_text(f"#!/bin/sh\n{text}\n")
+        (bare / name).chmod(0o755)
+    (bare / PACKAGE / "_fp8binding.so").write_bytes(b"of older sources")
+    python(bare, REFUSAL + f"""
+    import os, warnings
+    os.environ.update(HIPCC=os.path.abspath("hipcc"), CXX=os.path.abspath({cxx!r}))
+    from fp8_tensor_scaled_amd import build
+    with warnings.catch_warnings(record=True) as seen:
+        warnings.simplefilter("always")
+        lib = build.build()
+    assert os.path.exists(lib) and os.path.exists(build.BENCH_LIB)
+    said = [str(w.message) for w in seen if "_fp8binding" in str(w.message)]
+    assert len(said) == 1 and {"no headers here" if cxx == "failing" else "missing"!r} in said[0]
+    assert not os.path.exists(build.BINDING_LIB)
+    """)
+    python(bare, REFUSAL + """
+    import fp8_tensor_scaled_amd as f
+    assert f._take is f._take_slow
+    refuses(f)
     """)
