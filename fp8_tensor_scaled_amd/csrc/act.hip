@@ -6,11 +6,12 @@
 //
 // Sixteen lanes hold a group of 128 columns, eight each (and the same eight of
 // the other half): a step's maximum is theirs alone, 16-byte loads and stores
-// of a 2-byte type, no LDS.  A workgroup works on one set of groups: with two
-// rows a lane 16384 x 4096 gated bf16 took 95 us each way, with one 91.
+// of a 2-byte type, no LDS.  A workgroup works on one set of groups: two rows a
+// lane took 4 % longer at 16384 x 4096, gated bf16.
 //
-// Bandwidth bound: forward 16384 x 4096 gated bf16 with its checkpoint 91 us
-// (537 MB, 5.9 TB/s), backward 91.  The checkpoint, which is read much later, is
+// Bandwidth bound: forward 16384 x 4096 gated bf16 with its checkpoint 77 us
+// (541 MB, 7.0 TB/s), backward 89 (6.1 TB/s), calls in a row; 84 and 96 where each
+// ends before the next begins.  The checkpoint, which is read much later, is
 // written past the caches, y and dx, which the next operator reads, through
 // them (see written_early for smaller ones): with a block quantize of the output
 // behind it, forward 125 us and backward 167; with all written past the caches 135

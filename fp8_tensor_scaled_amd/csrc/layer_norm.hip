@@ -5,15 +5,21 @@
 // The variance is the mean of squared distances from the mean, not a
 // difference of two large sums.
 //
-// Bandwidth bound when large: 16384 x 4096 bf16 forward 49 us (268 MB, 5.5 TB/s),
-// backward 74 (403 MB and 8 MB of partial sums written and read, 5.6 TB/s); a
-// large copy reaches 5.0 to 5.2.  Small ones are bound by a row's chain (load, sums,
-// store): 2048 x 1024 forward 4 us, backward 8.5.
+// Bandwidth bound when large: 16384 x 4096 bf16 forward 50 us (268 MB, 5.4 TB/s),
+// backward 76 (403 MB and 8 MB of partial sums written and read, 5.5 TB/s); a
+// large copy reaches 5.0 to 5.2.  fp32: 102 and 153 us, 5.3 TB/s both.  Small ones are
+// bound by a row's chain (load, sums, store): 2048 x 1024 forward 4.0 us, backward
+// 8.3.  (Calls in a row; traced one by one 53, 71 + 5 and 5.2, 5.7 + 3.2.)
 //
 // A row is held in registers up to 16384 columns, by 8 to 32 lanes up to 256
 // columns, by a wave up to 1024, by several waves from there on; the columns' sums of the
 // backward stay in registers too, over all rows of a workgroup, and meet in LDS at
-// its end.  So x and g are read once.
+// its end.  So x and g are read once.  From 8193 columns on not all of the backward's
+// sums fit: the compiler puts 124 bytes a lane into memory for fp32 (204 where the
+// width is no multiple of 8) and 64 for the 2-byte types of such a width, none for
+// them otherwise.  4096 x 16384 forward / backward: bf16 60 / 84 us, 4.5 / 4.8 TB/s;
+// of 16383 columns 96 / 138, 2.8 / 2.9; fp32 115 / 219, 4.7 / 3.7; of 16383 129 /
+// 252, 4.2 / 3.2.
 
 #include "expert_block.hpp"
 #include "rows.hpp"
@@ -567,7 +573,12 @@ int64_t fwd_workgroups(int64_t rows) {
 
 // Backward: one for each CU (each is a share of the parameters' gradients to be
 // added up: with two 4096 x 8192 bf16 took 47 us, with one 41), and all go over
-// the same number of rows.
+// the same number of rows: where those are few turns, fewer workgroups, whose shares
+// are fewer to add up, take no longer than one on each CU with turns of uneven
+// number.  So / uneven, us, bf16: 257 places (2056 x 1024) 129 workgroups 8.4 / 8.4;
+// 288 (2300 x 1024) 8.6 / 9.3; 514 (4111 x 1000) 172 workgroups 11.0 / 11.7; 525 (4200 x
+// 1024) 10.9 / 11.6; 775 (6200 x 1024) 13.3 / 13.5; 1030 x 8192 19.6 / 21.6; dx alone
+// 257 places 4.8 / 4.3, 514 6.9 / 7.0.
 template <class S>
 int64_t bwd_workgroups(int64_t rows) {
     const int64_t need = workgroups_needed<S>(rows);
@@ -582,8 +593,10 @@ int64_t bwd_workgroups(int64_t rows) {
 // 21.7 / 32.5; 16384 x 2048 with 256 25.0 / 40.5, with 64 30.5 / 40.0; 4096 x 8192 with
 // 512 25.9 / 41.4, with 256 33.0 / 46.0; 2048 x 16384 with 512 33 / 47, with 1024 (which
 // have too few registers) 32 / 64.  Few rows of 4096 are shorter chains with 8 columns
-// a lane: 512 / 256 lanes 16 rows 3.2 / 4.0 forward, 2048 rows 8.4 / 10.3, 16384 rows
-// 53.6 / 49.7.
+// a lane.  512 / 256 lanes, forward: 16 rows 2.9 / 3.8, 2048 rows 7.8 / 9.9, 4096 rows
+// 15.3 / 16.8, 16384 rows 53.7 / 49.5; backward: 16 rows 2.9 / 3.3, 256 rows 5.1 / 4.4,
+// 1024 rows 13.4 / 13.3, 2048 rows 18.6 / 18.8, 4096 rows 25.4 / 24.6, 16384 rows 76.8 /
+// 75.9.
 constexpr int64_t kFewRows = 2048;
 template <bool WHOLE, class Fn>
 auto with_lanes(int64_t rows, int64_t cols, bool codes, Fn fn) {

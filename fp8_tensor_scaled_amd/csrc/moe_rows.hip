@@ -10,9 +10,12 @@
 // type, four of fp32), a wave 1 KB of it, or, where tokens are narrower, 16 or 32
 // of its lanes one each.  It has the loads of all choices under way before it
 // uses the first, so the number of choices is a template argument (the next of
-// 1, 2, 4, 8, 16).  Rows are read once: past the caches (combine 102 us, 119
-// without, at 131072 rows of 2048 bf16).  They are written through them, for the
-// next operator: dispatch of that size takes 111 us so and 102 past the caches,
+// 1, 2, 4, 8, 16: one of 3, 5, 6 or 7 of its own gains nothing there and in combine;
+// combine's backward with the next / its own, bf16: 2048 tokens of 1024, 3 choices
+// 7.0 / 6.8 us, 5 11.5 / 10.9, 6 13.1 / 12.5, 7 13.9 / 13.7; 16384 of 2048 94 / 93,
+// 149 / 149, 176 / 176, 207 / 208).  Rows are read once: past the caches (combine 102
+// us, 119 without, at 131072 rows of 2048 bf16).  They are written through them, for
+// the next operator: dispatch of that size takes 111 us so and 102 past the caches,
 // but with a block quantize of its rows behind it 249 and 277.
 
 #include "expert_block.hpp"

@@ -107,8 +107,11 @@ __global__ __launch_bounds__(kT) void sort_place_kernel(MoeSortLaunch p) {
     const Share s = share_of(p.pairs);
 
     if constexpr (MODE == kCounting) {
-        // neighbouring lanes count in copies of their own, so that few of them meet
-        // (16384 pairs of 7 experts 6.0 us, with one copy 7.3; of 64 6.1 and 5.8)
+        // neighbouring lanes count in copies of their own, so that few of them meet,
+        // which they do where experts are few; the copies' adding up costs the others
+        // as much.  16384 pairs, 16 copies / 8 / 1, us in a graph: 7 experts 6.0 / 5.9 /
+        // 7.6, 16 6.0 / 5.8 / 6.6, 32 6.0 / 5.8 / 5.8, 64 6.2 / 6.0 / 5.9, 255 6.8 / 6.5 /
+        // 6.2; 256 experts 6.7 with 8, 6.3 with 1.
         int* count = &of_wave[0][0];  // [2][copies][bins]
         const int copies = 2 * 16 * bins <= kWaves * kBins ? 16 : 8;
         for (int b = tid; b < 2 * copies * bins; b += kT) count[b] = 0;
