@@ -318,8 +318,10 @@ class FP8Experts(torch.nn.Module):
     top_k experts, weighted by the softmax of their logits (over the chosen
     ones with ``renormalize``, over all without).  Each expert is two
     ``FP8Linear`` layers around a gated silu, and takes its tokens as one run of
-    rows.  ``forward`` takes bf16 [..., dim]; it waits for the tokens' counts
-    (they are sizes of what follows), so it cannot be captured into a graph."""
+    rows; one without tokens takes no part in the batch, and its weights get no
+    gradient (None, not zeros).  ``forward`` takes bf16 [..., dim]; it waits for the
+    tokens' counts (they are sizes of what follows), so it cannot be captured into a
+    graph."""
 
     def __init__(self, dim: int, hidden: int, experts: int, top_k: int, renormalize: bool = True,
                  device=None, dtype=torch.bfloat16):
