@@ -680,7 +680,7 @@ fp8_status_t fp8_layer_norm_bwd(const void* g, const void* x, fp8_in_t type, int
  *
  * a(v) before its rounding to `type` is off by at most, in half steps of fp32
  * (2^-24 of the value): silu 6; gelu by tanh 6 + 12 |u|, the roundings of u in
- * fp32; gelu 12 + 1.5 v^2, those of v^2.  bf16 and fp16 inputs: 1.3 |v| (silu) or
+ * fp32; gelu 18 + 1.5 v^2, those of v^2.  bf16 and fp16 inputs: 1.3 |v| (silu) or
  * 2.6 |u| (gelu by tanh) more; 0 where v or 2u is below -88 (under 2^-120).
  *
  * x: row stride ldx.  rows, cols >= 0 (0: nothing happens).
